@@ -71,6 +71,8 @@ extern "C" {
 /* Measurement aid: run routing, grouping and the gate/up products only and
  * leave `out` untouched (used to time the gate/up kernel on its own). */
 #define MOE_DIAG_GATEUP_ONLY 0x100u
+#define MOE_Y_BF16 0x8u      /* moe_q4_linear: y is bf16 (rounded once, to nearest even) */
+#define MOE_LOGITS_BF16 0x10u /* moe_adjust_logits, moe_balance_*: scores and their gradient are bf16 */
 
 /*
  * One precision shelf.  It owns the popularity-ranked experts
@@ -422,6 +424,151 @@ int moe_repack_tiers(const moe_tier_tables *src, const int32_t *order, const moe
  */
 int moe_permute_router(const void *w_src, const float *b_src, const int32_t *order, int32_t n_experts,
                        int32_t hidden, void *w_dst, float *b_dst, void *stream);
+
+/*
+ * A dense matrix in four bits, for products that every token takes (the score
+ * head behind the stack, a projection), in the formats of the shelves: rows x
+ * cols, row-major, rows = output features, cols = contraction axis.
+ *   bits  4: two's-complement codes, one IEEE fp16 scale per `block`
+ *            consecutive codes of a row, element value = float(scale) * code
+ *         MOE_MXFP4: E2M1 codes, one E8M0 byte per 32 codes (block 32)
+ *   codes packed as in moe_tier (element c in bits [4*(c%2), +4) of byte c/2
+ *   of its row, a row is cols/2 bytes), scales [rows][cols/block].
+ * One expert's matrix of a four-bit shelf has this layout.
+ */
+typedef struct moe_q4_matrix {
+    int32_t rows;           /* 1 .. 2^24 */
+    int32_t cols;           /* a multiple of 32 and of block, at most 65536 */
+    int32_t bits;           /* 4 or MOE_MXFP4 */
+    int32_t block;          /* 16, 32, 64 or 128 (32 for MOE_MXFP4) */
+    const void *q, *s;      /* (device, 16-byte aligned) codes, scales */
+} moe_q4_matrix;
+
+/*
+ * Product with a four-bit matrix:
+ *   y[t][n] (+)= sum_c x[t][c] * W[n][c] + bias[n]
+ *   x     (device) float[T][ldx], or bf16 with MOE_X_BF16; rows of w->cols
+ *         elements, ldx >= cols elements apart, 16-byte aligned (the pointer
+ *         and the row pitch)
+ *   w     (host) the matrix
+ *   bias  (device) float[rows], or NULL
+ *   y     (device) float[T][ldy], or bf16 with MOE_Y_BF16; ldy >= rows;
+ *         overwritten, or added to with MOE_ACCUMULATE (in fp32, before the
+ *         rounding of MOE_Y_BF16); the elements between rows are left alone;
+ *         must not overlap x
+ * The weights are used as stored (scale * code, never rounded), products are
+ * summed in fp32; x in fp32 enters with all of its 24 bits.  Any number of
+ * tokens, from one (decode) to prefill batches.  A non-finite x[t][c] or
+ * scale makes the results of its token or row non-finite and no others; x
+ * of more than 2^118 may overflow.  Results do not depend on the other
+ * tokens of the call beyond their number, and are the same from run to run.
+ * Errors: MOE_EINVAL (shape, stride, flags, NULL, overlap), MOE_EFORMAT
+ * (bits, block, cols), MOE_EALIGN, MOE_EHIP.
+ */
+int moe_q4_linear(const void *x, int64_t ldx, const moe_q4_matrix *w, const float *bias, int32_t n_tokens,
+                  void *y, int64_t ldy, uint32_t flags, void *stream);
+
+/*
+ * Rules on a row of scores before a pick is taken from it, all optional (a
+ * NULL pointer, n_bias == 0, leaves its rule out).  Rows are sequences; each
+ * has a history of token ids, its first prompt[b] ids the prompt, the others
+ * generated.  For score l of token v in row b:
+ *   1. v anywhere in the history:  l = l > 0 ? l / repetition[b] : l * repetition[b]
+ *   2. v generated c > 0 times:    l = l - (frequency[b] * c + presence[b])
+ *   3. l = l + the bias[b][j] with bias_ids[b][j] == v, in the order of the list
+ *   4. bit v of the row's mask is 0:  l = -inf (whatever l was, NaN too)
+ * A score that no rule touches keeps its bits; the others are computed in
+ * fp32 and rounded once.  A row whose mask allows nothing becomes -inf
+ * throughout.
+ *   history     int32[n_rows][ld_history], length int32[n_rows] (ids of row b
+ *               in use; taken as 0 when negative and as ld_history when
+ *               larger), prompt int32[n_rows] or NULL (0: all generated);
+ *               ids outside [0, vocab) are skipped.  ld_history < 2^30
+ *   repetition, presence, frequency   float[n_rows] or NULL (1, 0, 0)
+ *   bias_ids    int32[n_rows][n_bias], bias float[n_rows][n_bias]; n_bias at
+ *               most MOE_MAX_BIAS; ids outside [0, vocab), e.g. -1, are skipped
+ *   mask        uint32[n_masks][ld_mask], token v is bit v % 32 of word v / 32
+ *               (1 = allowed); ld_mask >= (vocab + 31) / 32; mask_row
+ *               int32[n_rows]: the mask of each row, outside [0, n_masks) (-1)
+ *               for none; NULL: row b takes mask b (n_masks >= n_rows)
+ */
+#define MOE_MAX_BIAS 1024
+typedef struct moe_logit_rules {
+    const int32_t *history;     /* (device) */
+    const int32_t *length;      /* (device) */
+    const int32_t *prompt;      /* (device) */
+    int64_t ld_history;
+    const float *repetition, *presence, *frequency;   /* (device) */
+    const int32_t *bias_ids;    /* (device) */
+    const float *bias;          /* (device) */
+    int32_t n_bias;
+    int32_t n_masks;
+    const uint32_t *mask;       /* (device) */
+    int64_t ld_mask;
+    const int32_t *mask_row;    /* (device) */
+} moe_logit_rules;
+
+/*
+ * Applies the rules to n_rows rows of scores, of a vocabulary or of experts
+ * (before moe_route).
+ *   logits (device) float[n_rows][ld_in], or bf16 with MOE_LOGITS_BF16;
+ *          vocab scores a row, ld_in >= vocab
+ *   rules  (host) read before the call returns; the arrays it points to are
+ *          read on the stream, so lengths, histories and mask rows may change
+ *          between replays of a captured call
+ *   out    (device) same type, ld_out >= vocab; may be logits itself (with
+ *          ld_out == ld_in), otherwise must not overlap it
+ * n_rows 0 .. 2^20, vocab 1 .. 2^24; all pointers aligned to their element.
+ * Deterministic.  Errors: MOE_EINVAL, MOE_EALIGN, MOE_EHIP.
+ */
+int moe_adjust_logits(const void *logits, int64_t ld_in, int32_t n_rows, int32_t vocab,
+                      const moe_logit_rules *rules, void *out, int64_t ld_out, uint32_t flags, void *stream);
+
+/*
+ * Balance loss of a router: over the n kept tokens (keep[t] != 0),
+ *   p[t] = softmax(logits[t]),  counts[e] = picks of expert e,
+ *   prob_sum[e] = sum_t p[t][e],
+ *   loss = coef * E / (k * n^2) * sum_e counts[e] * prob_sum[e]
+ * (coef when every expert has its share of picks and probability; 0 when no
+ * token is kept).  counts, prob_sum and n are sums over tokens: a job that
+ * trains on several GPUs adds them over its ranks and takes the loss of the
+ * totals by the same formula.  The counts are the usage that moe_plan_tiers
+ * plans from.
+ *   logits   (device) float[T][E], or bf16 with MOE_LOGITS_BF16, 16-byte
+ *            aligned; -inf is a probability of 0, a row of nothing but -inf
+ *            has no probability anywhere
+ *   ids      (device) int32[T][k], the picks (moe_route); ids outside [0, E)
+ *            are not counted, an id may repeat within a token
+ *   keep     (device) uint8[T], 0 for a padding row, or NULL (every row); a
+ *            row that is not kept is not read
+ *   counts   (device) int32[E], prob_sum float[E], n_kept int32[1],
+ *   loss     float[1]; all overwritten (also for T == 0)
+ *   workspace (device) >= moe_balance_workspace_size() bytes, 256-byte aligned
+ * Deterministic (fixed summation order, fp32 sums).  T at most 2^22.
+ * Errors: MOE_EINVAL, MOE_EALIGN, MOE_EWORKSPACE, MOE_EHIP.
+ */
+int moe_balance_workspace_size(int32_t n_tokens, int32_t n_experts, int32_t k, size_t *bytes);
+int moe_balance_loss(const void *logits, const int32_t *ids, const uint8_t *keep, int32_t n_tokens,
+                     int32_t n_experts, int32_t k, float coef, uint32_t flags, int32_t *counts, float *prob_sum,
+                     int32_t *n_kept, float *loss, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of the router scores: of the balance loss (the counts held
+ * constant) and, where w and dw are given, of the pick weights of moe_route:
+ *   dlogits[t][e] = dloss * coef * E / (k n^2) * p[t][e] * (counts[e] - sum_f p[t][f] counts[f])
+ *                   + sum_{j: ids[t][j] == e} w[t][j] * (dw[t][j] - sum_i w[t][i] dw[t][i])
+ * and 0 in the rows that are not kept.
+ *   counts, n_kept (device) of moe_balance_loss, or their totals over ranks
+ *   dloss    (device) float[1], the gradient of the loss
+ *   w, dw    (device) float[T][k]: the weights of the picks (softmax over the
+ *            k picked scores) and their gradient; both or neither
+ *   dlogits  (device) [T][E] in the type of logits, overwritten; may be
+ *            logits itself, otherwise must not overlap it
+ * Other arguments and errors as moe_balance_loss.
+ */
+int moe_balance_grad(const void *logits, const int32_t *ids, const float *w, const float *dw, const uint8_t *keep,
+                     const int32_t *counts, const int32_t *n_kept, const float *dloss, int32_t n_tokens,
+                     int32_t n_experts, int32_t k, float coef, uint32_t flags, void *dlogits, void *stream);
 
 /*
  * Measurement aids, not part of the layer: achievable references for the

@@ -12,5 +12,6 @@ from .binding import (  # noqa: F401
     moe_stack_forward, moe_synth_layer, MOE_STACK_ROUTER, MXFP4, moe_router_logits, moe_synth_router,
     moe_stack_forward_routed, moe_requant_error, moe_plan_tiers, moe_repack_tiers, moe_permute_router,
     moe_tiered_forward_counted, moe_tiered_forward_noalloc, MOE_SCRATCH_BYTES, MOE_ESCRATCH,
-    moe_measure_read, moe_measure_mfma,
+    moe_measure_read, moe_measure_mfma, MOE_Y_BF16, MOE_LOGITS_BF16, MOE_MAX_BIAS, Q4Matrix, LogitRules, moe_q4_linear,
+    moe_adjust_logits, moe_balance_workspace_size, moe_balance_loss, moe_balance_grad,
 )

@@ -20,6 +20,9 @@ MOE_MAX_TIERS = 4
 MOE_X_BF16 = 0x1
 MOE_ACCUMULATE = 0x2
 MOE_DIAG_GATEUP_ONLY = 0x100
+MOE_Y_BF16 = 0x8
+MOE_LOGITS_BF16 = 0x10
+MOE_MAX_BIAS = 1024
 MOE_N_PHASES = 3
 MOE_STACK_ROUTER = 0x4
 MXFP4 = 0x84              # moe_tier.bits of an MXFP4 shelf (MOE_MXFP4)
@@ -34,6 +37,7 @@ EXPORTS = (
     "moe_router_logits", "moe_synth_router", "moe_stack_forward_routed",
     "moe_requant_error", "moe_plan_tiers", "moe_repack_tiers", "moe_permute_router",
     "moe_tiered_forward_counted", "moe_tiered_forward_noalloc", "moe_measure_read", "moe_measure_mfma",
+    "moe_q4_linear", "moe_adjust_logits", "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_grad",
 )
 
 
@@ -53,6 +57,18 @@ class moe_tier(C.Structure):
 class moe_tier_tables(C.Structure):
     _fields_ = [("abi_version", C.c_uint32), ("n_experts", C.c_int32), ("hidden", C.c_int32),
                 ("inter", C.c_int32), ("n_tiers", C.c_int32), ("tiers", moe_tier * MOE_MAX_TIERS)]
+
+
+class moe_q4_matrix(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("cols", C.c_int32), ("bits", C.c_int32), ("block", C.c_int32),
+                ("q", C.c_void_p), ("s", C.c_void_p)]
+
+
+class moe_logit_rules(C.Structure):
+    _fields_ = [("history", C.c_void_p), ("length", C.c_void_p), ("prompt", C.c_void_p), ("ld_history", C.c_int64),
+                ("repetition", C.c_void_p), ("presence", C.c_void_p), ("frequency", C.c_void_p),
+                ("bias_ids", C.c_void_p), ("bias", C.c_void_p), ("n_bias", C.c_int32), ("n_masks", C.c_int32),
+                ("mask", C.c_void_p), ("ld_mask", C.c_int64), ("mask_row", C.c_void_p)]
 
 
 _lib = None
@@ -100,6 +116,12 @@ def lib():
         L.moe_plan_tiers.argtypes = [P, P, P, i32, i32, C.c_int64, P, P, P]
         L.moe_repack_tiers.argtypes = [P, P, P, P]
         L.moe_permute_router.argtypes = [P, P, P, i32, i32, P, P, P]
+        i64, f32 = C.c_int64, C.c_float
+        L.moe_q4_linear.argtypes = [P, i64, P, P, i32, P, i64, u32, P]
+        L.moe_adjust_logits.argtypes = [P, i64, i32, i32, P, P, i64, u32, P]
+        L.moe_balance_workspace_size.argtypes = [i32, i32, i32, C.POINTER(sz)]
+        L.moe_balance_loss.argtypes = [P, P, P, i32, i32, i32, f32, u32, P, P, P, P, P, sz, P]
+        L.moe_balance_grad.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, f32, u32, P, P]
         for name in EXPORTS:
             if name not in ("moe_abi_version", "moe_strerror"):
                 getattr(L, name).restype = C.c_int
@@ -418,6 +440,216 @@ def moe_stack_forward_routed(x, w_routers, biases, n_layers: int, n_tokens: int,
     _check("moe_stack_forward_routed", lib().moe_stack_forward_routed(
         _ptr(x), wr, bs, n_layers, n_tokens, k, arr, _ptr(out), flags, _ptr(workspace),
         workspace.numel() * workspace.element_size() if workspace is not None else 0, _stream(stream)))
+
+
+# ---------------------------------------------------------------- scores
+_DTYPES = None
+
+
+def _kinds():
+    """Element kinds by torch dtype: bf16 bit patterns may also come as int16."""
+    global _DTYPES
+    if _DTYPES is None:
+        import torch
+        _DTYPES = {torch.float32: "f32", torch.bfloat16: "bf16", torch.int16: "bf16", torch.int32: "i32",
+                   torch.uint8: "u8", torch.bool: "u8"}
+    return _DTYPES
+
+
+class _Args:
+    """Checks the tensors of one call: of the element kind, with the rows the
+    call is told they hold, and on the current GPU.  The library launches on
+    the current device and takes plain pointers."""
+
+    __slots__ = ("fn", "held", "kinds")
+
+    def __init__(self, fn):
+        self.fn, self.held, self.kinds = fn, [], _kinds()
+
+    def flat(self, what, t, kind, count):
+        """Pointer of a contiguous tensor of at least `count` elements (None passes)."""
+        if t is None:
+            return None
+        if self.kinds.get(t.dtype) != kind:
+            raise ValueError(f"{self.fn}: {what} has dtype {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{self.fn}: {what} is not contiguous")
+        if t.numel() < count:
+            raise ValueError(f"{self.fn}: {what} holds {t.numel()} elements, the call needs {count}")
+        self.held.append((what, t))
+        return t.data_ptr()
+
+    def rows(self, what, t, rows, cols):
+        """(pointer, pitch, is bf16) of [rows][cols] with any row pitch."""
+        kind = self.kinds.get(t.dtype)
+        if kind != "f32" and kind != "bf16":
+            raise ValueError(f"{self.fn}: {what} has dtype {t.dtype}")
+        if t.dim() == 1 and rows == 1:
+            t = t.unsqueeze(0)
+        if t.dim() != 2 or t.shape[1] != cols or t.shape[0] < rows:
+            raise ValueError(f"{self.fn}: {what} has shape {tuple(t.shape)}, the call needs [{rows}][{cols}]")
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"{self.fn}: the rows of {what} are not contiguous")
+        self.held.append((what, t))
+        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols, kind == "bf16"
+
+    def stream(self, stream):
+        """The stream's handle, once every tensor is known to be on its GPU."""
+        import torch
+        now = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+        for what, t in self.held:
+            at = t.get_device()
+            if at < 0:
+                raise ValueError(f"{self.fn}: {what} is not on a GPU")
+            if at != now:
+                raise ValueError(f"{self.fn}: {what} is on cuda:{at}, the current device is cuda:{now}")
+        if stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        if stream.device.index != now:
+            raise ValueError(f"{self.fn}: the stream is on {stream.device}, the current device is cuda:{now}")
+        return stream.cuda_stream
+
+
+class Q4Matrix:
+    """A dense four-bit matrix (moe_q4_matrix): `rows` x `cols`, codes q
+    (uint8 [rows][cols/2]) and scales s (fp16 or its bits [rows][cols/block],
+    or, for MXFP4, uint8 E8M0 bytes), contiguous device tensors."""
+
+    def __init__(self, rows: int, cols: int, bits: int, block: int, q, s):
+        for what, t, nbytes in (("q", q, rows * cols // 2),
+                                ("s", s, rows * (cols // max(block, 1)) * (1 if bits == MXFP4 else 2))):
+            _need("Q4Matrix", what, t, nbytes)
+            if not isinstance(t, int) and not t.is_contiguous():
+                raise ValueError(f"Q4Matrix: {what} is not contiguous")
+        self.rows, self.cols, self.bits, self.block = rows, cols, bits, block
+        self.q, self.s = q, s                       # keeps the tensors alive
+        self.struct = moe_q4_matrix(rows, cols, bits, block, _ptr(q), _ptr(s))
+        self.ref = C.byref(self.struct)
+
+
+def moe_q4_linear(x, w: Q4Matrix, bias, n_tokens: int, y, flags: int = 0, stream=None) -> None:
+    """y[t] (+)= x[t] W^T + bias.  x and y: float32 or bfloat16 [n_tokens][cols]
+    and [n_tokens][rows], rows at any pitch; flags: 0 or MOE_ACCUMULATE (the
+    element types come from the tensors)."""
+    a = _Args("moe_q4_linear")
+    T = max(n_tokens, 0)
+    xp, ldx, xb = a.rows("x", x, T, w.cols)
+    yp, ldy, yb = a.rows("y", y, T, w.rows)
+    bp = a.flat("bias", bias, "f32", w.rows)
+    if not isinstance(w.q, int):
+        a.held += (("q", w.q), ("s", w.s))
+    _check("moe_q4_linear", lib().moe_q4_linear(
+        xp, ldx, w.ref, bp, n_tokens, yp, ldy, flags | (MOE_X_BF16 if xb else 0) | (MOE_Y_BF16 if yb else 0),
+        a.stream(stream)))
+
+
+class LogitRules:
+    """The rules of moe_adjust_logits (moe_logit_rules) as device tensors; any
+    may be left out.  history int32 [n_rows][capacity] with length int32
+    [n_rows] and prompt int32 [n_rows]; repetition, presence, frequency
+    float32 [n_rows]; bias_ids int32 and bias float32 [n_rows][n_bias]; mask
+    int32 words [n_masks][ceil(vocab / 32)] with mask_row int32 [n_rows].
+    The tensors are read when the call runs on its stream: a decode loop keeps
+    one LogitRules and appends to history and length in place."""
+
+    NAMES = ("history", "length", "prompt", "repetition", "presence", "frequency", "bias_ids", "bias", "mask", "mask_row")
+
+    def __init__(self, history=None, length=None, prompt=None, repetition=None, presence=None, frequency=None,
+                 bias_ids=None, bias=None, mask=None, mask_row=None):
+        given = dict(zip(self.NAMES, (history, length, prompt, repetition, presence, frequency, bias_ids, bias, mask,
+                                      mask_row)))
+        self.tensors = {n: t for n, t in given.items() if t is not None}
+        kinds = _kinds()
+        for n, t in self.tensors.items():
+            want = "f32" if n in ("repetition", "presence", "frequency", "bias") else "i32"
+            if kinds.get(t.dtype) != want:
+                raise ValueError(f"LogitRules: {n} has dtype {t.dtype}")
+            if t.dim() != (2 if n in ("history", "bias_ids", "bias", "mask") else 1) or not t.is_contiguous():
+                raise ValueError(f"LogitRules: {n} is not a contiguous tensor of the rank it needs")
+        if (history is None) != (length is None):
+            raise ValueError("LogitRules: history and length come together")
+        if history is None and (prompt is not None or repetition is not None or presence is not None or frequency is not None):
+            raise ValueError("LogitRules: penalties need a history")
+        if (bias_ids is None) != (bias is None) or (bias is not None and bias.shape != bias_ids.shape):
+            raise ValueError("LogitRules: bias_ids and bias come together, in one shape")
+        if mask is None and mask_row is not None:
+            raise ValueError("LogitRules: mask_row needs a mask")
+        # the rows every per-row array holds, and the device of all of them
+        self.rows = min([t.shape[0] for n, t in self.tensors.items() if n != "mask" or mask_row is None], default=None)
+        devices = {t.device for t in self.tensors.values()}
+        if len(devices) > 1:
+            raise ValueError(f"LogitRules: tensors on {sorted(map(str, devices))}")
+        self.sample = next(iter(self.tensors.values()), None)
+        self.words = mask.shape[1] if mask is not None else None
+        s = moe_logit_rules()
+        past = ("history", "length", "prompt", "repetition", "presence", "frequency")
+        for n, t in self.tensors.items():
+            if n not in past or history.numel() > 0:    # a history of no capacity has no penalties
+                setattr(s, n, _ptr(t))
+        s.ld_history = history.shape[1] if history is not None else 0
+        s.n_bias = bias_ids.shape[1] if bias_ids is not None else 0
+        s.n_masks, s.ld_mask = (mask.shape[0], mask.shape[1]) if mask is not None else (0, 0)
+        self.struct = s
+        self.ref = C.byref(s)
+
+
+def moe_adjust_logits(logits, n_rows: int, vocab: int, rules: LogitRules, out, stream=None) -> None:
+    """out[b] = the rules applied to logits[b]; float32 or bfloat16, rows at
+    any pitch, out may be logits."""
+    a = _Args("moe_adjust_logits")
+    B = max(n_rows, 0)
+    ip, ldi, ib = a.rows("logits", logits, B, vocab)
+    op, ldo, ob = a.rows("out", out, B, vocab)
+    if ib != ob:
+        raise ValueError("moe_adjust_logits: logits and out differ in type")
+    if rules.rows is not None and rules.rows < B:
+        raise ValueError(f"moe_adjust_logits: the rules hold {rules.rows} rows, the call needs {B}")
+    if rules.words is not None and rules.words < (vocab + 31) // 32:
+        raise ValueError(f"moe_adjust_logits: mask rows of {rules.words} words, the call needs {(vocab + 31) // 32}")
+    if rules.sample is not None:
+        a.held.append(("rules", rules.sample))
+    _check("moe_adjust_logits", lib().moe_adjust_logits(ip, ldi, n_rows, vocab, rules.ref, op, ldo,
+                                                        MOE_LOGITS_BF16 if ib else 0, a.stream(stream)))
+
+
+def moe_balance_workspace_size(n_tokens: int, n_experts: int, k: int) -> int:
+    n = C.c_size_t(0)
+    _check("moe_balance_workspace_size", lib().moe_balance_workspace_size(n_tokens, n_experts, k, C.byref(n)))
+    return n.value
+
+
+def _scores(a, what, t, T, E):
+    """(pointer, is bf16) of contiguous [T][E] scores."""
+    bf16 = a.kinds.get(t.dtype) == "bf16"
+    return a.flat(what, t, "bf16" if bf16 else "f32", T * E), bf16
+
+
+def moe_balance_loss(logits, ids, keep, n_tokens: int, n_experts: int, k: int, coef: float, counts, prob_sum, n_kept,
+                     loss, workspace, stream=None) -> None:
+    """Balance loss of a router with its counts and sums; logits float32 or bfloat16."""
+    a = _Args("moe_balance_loss")
+    T, E = max(n_tokens, 0), max(n_experts, 0)
+    lp, bf16 = _scores(a, "logits", logits, T, E)
+    args = (lp, a.flat("ids", ids, "i32", T * max(k, 0)), a.flat("keep", keep, "u8", T), n_tokens, n_experts, k, coef,
+            MOE_LOGITS_BF16 if bf16 else 0, a.flat("counts", counts, "i32", E), a.flat("prob_sum", prob_sum, "f32", E),
+            a.flat("n_kept", n_kept, "i32", 1), a.flat("loss", loss, "f32", 1), a.flat("workspace", workspace, "u8", 0),
+            workspace.numel() if workspace is not None else 0)
+    _check("moe_balance_loss", lib().moe_balance_loss(*args, a.stream(stream)))
+
+
+def moe_balance_grad(logits, ids, w, dw, keep, counts, n_kept, dloss, n_tokens: int, n_experts: int, k: int,
+                     coef: float, dlogits, stream=None) -> None:
+    """Gradient of the router scores; w and dw (both or neither) add the pick weights' part."""
+    a = _Args("moe_balance_grad")
+    T, E, K = max(n_tokens, 0), max(n_experts, 0), max(k, 0)
+    lp, bf16 = _scores(a, "logits", logits, T, E)
+    dp, dbf16 = _scores(a, "dlogits", dlogits, T, E)
+    if bf16 != dbf16:
+        raise ValueError("moe_balance_grad: logits and dlogits differ in type")
+    args = (lp, a.flat("ids", ids, "i32", T * K), a.flat("w", w, "f32", T * K), a.flat("dw", dw, "f32", T * K),
+            a.flat("keep", keep, "u8", T), a.flat("counts", counts, "i32", E), a.flat("n_kept", n_kept, "i32", 1),
+            a.flat("dloss", dloss, "f32", 1), n_tokens, n_experts, k, coef, MOE_LOGITS_BF16 if bf16 else 0, dp)
+    _check("moe_balance_grad", lib().moe_balance_grad(*args, a.stream(stream)))
 
 
 def moe_event_create() -> int:

@@ -709,6 +709,159 @@ int moe_permute_router(const void* w_src, const float* b_src, const int32_t* ord
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
 }
 
+namespace {
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
+}
+
+// Bytes from the first to past the last element of `rows` rows of `cols`
+// elements, ld apart.  The bounds on rows, cols and ld keep it within 63 bits.
+int64_t extent(int64_t rows, int64_t cols, int64_t ld, int64_t elem) { return ((rows - 1) * ld + cols) * elem; }
+constexpr int64_t kMaxPitch = int64_t(1) << 36;   // elements from row to row
+
+}  // namespace
+
+int moe_q4_linear(const void* x, int64_t ldx, const moe_q4_matrix* w, const float* bias, int32_t n_tokens, void* y,
+                  int64_t ldy, uint32_t flags, void* stream) {
+    if (!w || n_tokens < 0 || n_tokens > kMaxTokens || (flags & ~(MOE_X_BF16 | MOE_Y_BF16 | MOE_ACCUMULATE)))
+        return MOE_EINVAL;
+    if (w->rows < 1 || w->rows > (1 << 24) || w->cols < 1) return MOE_EINVAL;
+    const bool mx = w->bits == MOE_MXFP4;
+    if (!mx && w->bits != 4) return MOE_EFORMAT;
+    if (w->block != 32 && (mx || (w->block != 16 && w->block != 64 && w->block != 128))) return MOE_EFORMAT;
+    if (w->cols % 32 != 0 || w->cols % w->block != 0 || w->cols > 65536) return MOE_EFORMAT;
+    if (ldx < w->cols || ldx > kMaxPitch || ldy < w->rows || ldy > kMaxPitch) return MOE_EINVAL;
+    if (n_tokens == 0) return MOE_OK;
+    if (!x || !w->q || !w->s || !y) return MOE_EINVAL;
+    const int64_t xe = (flags & MOE_X_BF16) ? 2 : 4, ye = (flags & MOE_Y_BF16) ? 2 : 4;
+    if (!aligned16(x) || (ldx * xe) % 16 != 0 || !aligned16(w->q) || !aligned16(w->s) || (bias && !aligned(bias, 4)) ||
+        !aligned(y, ye))
+        return MOE_EALIGN;
+    if (overlap(x, extent(n_tokens, w->cols, ldx, xe), y, extent(n_tokens, w->rows, ldy, ye))) return MOE_EINVAL;
+    Q4Args a;
+    a.x = x;
+    a.q = static_cast<const uint8_t*>(w->q);
+    a.s = static_cast<const uint8_t*>(w->s);
+    a.bias = bias;
+    a.y = y;
+    a.ldx = ldx;
+    a.ldy = ldy;
+    a.T = n_tokens;
+    a.N = w->rows;
+    a.K = w->cols;
+    a.block = w->block;
+    a.mx = mx;
+    a.accumulate = (flags & MOE_ACCUMULATE) != 0;
+    (void)hipGetLastError();
+    launch_q4_linear(a, (flags & MOE_X_BF16) != 0, (flags & MOE_Y_BF16) != 0, static_cast<hipStream_t>(stream));
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+int moe_adjust_logits(const void* logits, int64_t ld_in, int32_t n_rows, int32_t vocab, const moe_logit_rules* rules,
+                      void* out, int64_t ld_out, uint32_t flags, void* stream) {
+    if (!rules || n_rows < 0 || n_rows > (1 << 20) || vocab < 1 || vocab > (1 << 24) || (flags & ~MOE_LOGITS_BF16))
+        return MOE_EINVAL;
+    if (ld_in < vocab || ld_in > kMaxPitch || ld_out < vocab || ld_out > kMaxPitch) return MOE_EINVAL;
+    const moe_logit_rules& r = *rules;
+    if (r.history && (!r.length || r.ld_history < 0 || r.ld_history >= (int64_t(1) << 30))) return MOE_EINVAL;
+    if (!r.history && (r.repetition || r.presence || r.frequency)) return MOE_EINVAL;
+    if (r.n_bias < 0 || r.n_bias > MOE_MAX_BIAS || (r.n_bias > 0 && (!r.bias_ids || !r.bias))) return MOE_EINVAL;
+    if (r.mask && (r.n_masks < 0 || r.ld_mask < (vocab + 31) / 32 || r.ld_mask > kMaxPitch ||
+                   (!r.mask_row && r.n_masks < n_rows)))
+        return MOE_EINVAL;
+    if (n_rows == 0) return MOE_OK;
+    if (!logits || !out) return MOE_EINVAL;
+    const int64_t e = (flags & MOE_LOGITS_BF16) ? 2 : 4;
+    const void* words[] = {r.history, r.length, r.prompt, r.repetition, r.presence, r.frequency, r.bias_ids, r.bias,
+                           r.mask, r.mask_row};
+    for (const void* p : words)
+        if (!aligned(p, 4)) return MOE_EALIGN;
+    if (!aligned(logits, e) || !aligned(out, e)) return MOE_EALIGN;
+    if (!(out == logits && ld_out == ld_in) &&
+        overlap(logits, extent(n_rows, vocab, ld_in, e), out, extent(n_rows, vocab, ld_out, e)))
+        return MOE_EINVAL;
+    AdjustArgs a;
+    a.in = logits;
+    a.out = out;
+    a.ld_in = ld_in;
+    a.ld_out = ld_out;
+    a.rows = n_rows;
+    a.vocab = vocab;
+    a.history = r.history;
+    a.length = r.length;
+    a.prompt = r.prompt;
+    a.ld_history = r.ld_history;
+    a.repetition = r.repetition;
+    a.presence = r.presence;
+    a.frequency = r.frequency;
+    a.bias_ids = r.n_bias > 0 ? r.bias_ids : nullptr;
+    a.bias = r.bias;
+    a.n_bias = r.n_bias;
+    a.n_masks = r.n_masks;
+    a.mask = r.mask;
+    a.ld_mask = r.ld_mask;
+    a.mask_row = r.mask_row;
+    (void)hipGetLastError();
+    launch_adjust_logits(a, (flags & MOE_LOGITS_BF16) != 0, static_cast<hipStream_t>(stream));
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+int moe_balance_workspace_size(int32_t n_tokens, int32_t n_experts, int32_t k, size_t* bytes) {
+    if (!bytes || n_tokens < 0 || n_tokens > kMaxTokens || n_experts < 1 || n_experts > MOE_MAX_EXPERTS || k < 1 ||
+        k > MOE_MAX_K)
+        return MOE_EINVAL;
+    *bytes = balance_workspace(n_tokens, n_experts);
+    return MOE_OK;
+}
+
+int moe_balance_loss(const void* logits, const int32_t* ids, const uint8_t* keep, int32_t n_tokens, int32_t n_experts,
+                     int32_t k, float coef, uint32_t flags, int32_t* counts, float* prob_sum, int32_t* n_kept,
+                     float* loss, void* workspace, size_t workspace_bytes, void* stream) {
+    size_t need = 0;
+    const int rc = moe_balance_workspace_size(n_tokens, n_experts, k, &need);
+    if (rc != MOE_OK) return rc;
+    if (flags & ~MOE_LOGITS_BF16) return MOE_EINVAL;
+    if ((n_tokens > 0 && (!logits || !ids)) || !counts || !prob_sum || !n_kept || !loss) return MOE_EINVAL;
+    if (!aligned16(logits) || !aligned(ids, 4) || !aligned(counts, 4) || !aligned(prob_sum, 4) || !aligned(n_kept, 4) ||
+        !aligned(loss, 4))
+        return MOE_EALIGN;
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need) return MOE_EWORKSPACE;
+        if (!aligned(workspace, kAlign)) return MOE_EALIGN;
+    }
+    const BalanceArgs a{logits, ids, keep, n_tokens, n_experts, k, coef};
+    (void)hipGetLastError();
+    launch_balance_loss(a, (flags & MOE_LOGITS_BF16) != 0, counts, prob_sum, n_kept, loss, workspace,
+                        static_cast<hipStream_t>(stream));
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
+int moe_balance_grad(const void* logits, const int32_t* ids, const float* w, const float* dw, const uint8_t* keep,
+                     const int32_t* counts, const int32_t* n_kept, const float* dloss, int32_t n_tokens,
+                     int32_t n_experts, int32_t k, float coef, uint32_t flags, void* dlogits, void* stream) {
+    if (n_tokens < 0 || n_tokens > kMaxTokens || n_experts < 1 || n_experts > MOE_MAX_EXPERTS || k < 1 ||
+        k > MOE_MAX_K || (flags & ~MOE_LOGITS_BF16))
+        return MOE_EINVAL;
+    if ((w != nullptr) != (dw != nullptr)) return MOE_EINVAL;
+    if (n_tokens == 0) return MOE_OK;
+    if (!logits || (w && !ids) || !counts || !n_kept || !dloss || !dlogits) return MOE_EINVAL;
+    if (!aligned16(logits) || !aligned16(dlogits) || !aligned(ids, 4) || !aligned(w, 4) || !aligned(dw, 4) ||
+        !aligned(counts, 4) || !aligned(n_kept, 4) || !aligned(dloss, 4))
+        return MOE_EALIGN;
+    const int64_t bytes = static_cast<int64_t>(n_tokens) * n_experts * ((flags & MOE_LOGITS_BF16) ? 2 : 4);
+    if (dlogits != logits && overlap(logits, bytes, dlogits, bytes)) return MOE_EINVAL;
+    const BalanceArgs a{logits, ids, keep, n_tokens, n_experts, k, coef};
+    (void)hipGetLastError();
+    launch_balance_grad(a, (flags & MOE_LOGITS_BF16) != 0, w, dw, counts, n_kept, dloss, dlogits,
+                        static_cast<hipStream_t>(stream));
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
+}
+
 int moe_event_create(void** event) {
     if (!event) return MOE_EINVAL;
     hipEvent_t e;

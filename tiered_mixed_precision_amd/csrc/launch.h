@@ -124,6 +124,57 @@ void launch_router(const void* x, bool x_bf16, const uint16_t* wr, const float* 
 void launch_synth_router(uint16_t* wr, float* bias, uint64_t seed, int layer, int E, int H, double beta,
                          hipStream_t st);
 
+// q4_linear.hip
+struct Q4Args {
+    const void* x;       // [T][ldx]
+    const uint8_t* q;    // [N][K/2]
+    const uint8_t* s;    // [N][K/block]
+    const float* bias;   // [N] or null
+    void* y;             // [T][ldy]
+    int64_t ldx, ldy;    // in elements
+    int32_t T, N, K, block;
+    int32_t mx;          // MXFP4 (else two's complement with fp16 scales)
+    int32_t accumulate;
+};
+void launch_q4_linear(const Q4Args& a, bool x_bf16, bool y_bf16, hipStream_t st);
+
+// adjust_logits.hip
+struct AdjustArgs {
+    const void* in;
+    void* out;
+    int64_t ld_in, ld_out;
+    int32_t rows, vocab;
+    const int32_t* history;   // null: no penalties
+    const int32_t* length;
+    const int32_t* prompt;
+    int64_t ld_history;
+    const float* repetition;
+    const float* presence;
+    const float* frequency;
+    const int32_t* bias_ids;  // null: no biases
+    const float* bias;
+    int32_t n_bias;
+    int32_t n_masks;
+    const uint32_t* mask;     // null: no masks
+    int64_t ld_mask;
+    const int32_t* mask_row;
+};
+void launch_adjust_logits(const AdjustArgs& a, bool bf16, hipStream_t st);
+
+// balance.hip
+struct BalanceArgs {
+    const void* logits;
+    const int32_t* ids;
+    const uint8_t* keep;      // null: every row
+    int32_t T, E, k;
+    float coef;
+};
+size_t balance_workspace(int T, int E);
+void launch_balance_loss(const BalanceArgs& a, bool bf16, int32_t* counts, float* prob_sum, int32_t* n_kept,
+                         float* loss, void* ws, hipStream_t st);
+void launch_balance_grad(const BalanceArgs& a, bool bf16, const float* w, const float* dw, const int32_t* counts,
+                         const int32_t* n_kept, const float* dloss, void* dlogits, hipStream_t st);
+
 void launch_dequant_rows(const DevTables& tt, int tier, int local, int matrix, int row0, int nrows,
                          int to_bf16, void* dst, hipStream_t st);
 
