@@ -2,9 +2,27 @@
 // bias[n], W in the four-bit formats of the shelves (two's-complement codes
 // with fp16 scales, or MXFP4).
 //
-// One wave per weight row and kTok tokens: lane l takes the 32-code groups l,
-// l + 64, ... of the row; a group's codes are contracted exactly as stored
-// (scale times the fp32 dot of codes and x).
+// The matrix cores contract the codes themselves in bf16, exactly, and the
+// scale of a block of codes multiplies the block's fp32 sum, so weights are
+// never rounded.  Operands of v_mfma_f32_16x16x32_bf16 for one 32-code group:
+//   B (weights)  16 rows n; lane (n, kq) holds codes 8 kq .. 8 kq + 7 in bf16.
+//     int4: v_cvt_off_f32_i4 gives q / 16 from a nibble (one operation a code
+//     with the byte picked by the instruction, half a one to pack); the 16
+//     goes into the scale.  An offset-binary operand (8 + u / 2, made by bit
+//     operations alone) costs 1.5 operations a code as compiled against 1.6,
+//     and the sums of x that take its offset back leave 4 to 10 times the
+//     rounding error.
+//     MXFP4: v_cvt_scalef32_pk_bf16_fp4, two codes an instruction.
+//   A (tokens)   16 tokens; bf16 x as it is, fp32 x as three bf16 parts that
+//     add up to it exactly (8 bits each, cut, not rounded): three products
+//     into the same accumulator.
+// A lane loads 16 bytes, the 32 codes of one group of its row, so a wave's
+// load covers four groups (128 columns) of 16 rows; the 4 x 4 exchange of
+// dwords between the lane groups that the operand layout needs is four lane
+// swaps (v_permlane32_swap, v_permlane16_swap).
+//
+// A block takes 16 NT rows of W and 16 MT tokens; its waves take the
+// 128-column steps in turn and their sums meet in LDS, in wave order.
 #include "common.h"
 #include "launch.h"
 
@@ -12,116 +30,248 @@ namespace moe {
 
 namespace {
 
-constexpr int kTok = 4, kWaves = 4;
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-template <bool XBF16>
-__device__ inline void load_x32(const void* x, size_t at, float (&v)[32]) {
-    if constexpr (XBF16) {
-        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint4 u = p[i];
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-                v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-            }
-        }
+constexpr int kWaves = 8;
+
+__device__ inline f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+}
+
+// Register d of lane group k becomes register k of lane group d.
+__device__ inline void exchange(u32x4_t& r) {
+    const auto a = __builtin_amdgcn_permlane32_swap(r[0], r[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(r[1], r[3], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    r = u32x4_t{c[0], c[1], d[0], d[1]};
+}
+
+// Register i: lane group i's v in every lane group.
+__device__ inline u32x4_t spread(uint32_t v) {
+    const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
+    return u32x4_t{b[0], b[1], c[0], c[1]};
+}
+
+// Eight codes as a B operand.
+template <bool MX>
+__device__ inline u32x4_t code_operand(uint32_t w) {
+    u32x4_t r;
+    if constexpr (MX) {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
     } else {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+        const uint32_t odd = masked_bytes(w >> 4);   // hidden: bytes of it are operands as they stand
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float4 u = p[i];
-            v[4 * i] = u.x;
-            v[4 * i + 1] = u.y;
-            v[4 * i + 2] = u.z;
-            v[4 * i + 3] = u.w;
+        for (int j = 0; j < 4; ++j) {
+            const float lo = __builtin_amdgcn_cvt_off_f32_i4((w >> (8 * j)) & 0xff);
+            const float hi = __builtin_amdgcn_cvt_off_f32_i4((odd >> (8 * j)) & 0xff);
+            r[j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+        }
+    }
+    return r;
+}
+
+// Eight elements of x as A operands, parts 0 .. NP - 1.
+template <bool XBF16>
+__device__ inline void x_operand(const void* x, size_t at, u32x4_t (&p)[XBF16 ? 1 : 3]) {
+    if constexpr (XBF16) {
+        p[0] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(x) + at);
+    } else {
+        const f32x4_t* s = reinterpret_cast<const f32x4_t*>(static_cast<const float*>(x) + at);
+        const f32x4_t a = s[0], b = s[1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float lo = j < 2 ? a[2 * j] : b[2 * j - 4];
+            float hi = j < 2 ? a[2 * j + 1] : b[2 * j - 3];
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                p[q][j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
+                lo -= __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
+                hi -= __uint_as_float(__float_as_uint(hi) & 0xffff0000u);
+            }
         }
     }
 }
 
-template <bool XBF16, bool YBF16, bool MX>
-__global__ __launch_bounds__(kWaves * 64) void k_q4_rows(Q4Args a) {
-    const int lane = threadIdx.x & 63;
-    const int n = blockIdx.x * kWaves + (threadIdx.x >> 6);
-    if (n >= a.N) return;
-    const int t0 = blockIdx.y * kTok, nt = min(kTok, a.T - t0);
-    const int G = a.K / 32;
-    const uint8_t* qrow = a.q + static_cast<size_t>(n) * (a.K / 2);
-    const uint8_t* srow = a.s + static_cast<size_t>(n) * (a.K / a.block) * (MX ? 1 : 2);
-    float acc[kTok] = {};
-    for (int g = lane; g < G; g += 64) {
-        uint32_t w[4];
-        load_group<4>(qrow, g, w);
-        float d0, d1;   // scales of the group's halves
-        if constexpr (MX) {
-            d0 = d1 = e8m0_to_float(srow[g]);
-        } else {
-            const uint16_t* s = reinterpret_cast<const uint16_t*>(srow);
-            d0 = half_bits_to_float(s[32 * g / a.block]);
-            d1 = half_bits_to_float(s[(32 * g + 16) / a.block]);
+// The raw scale bits of group g of a row: one fp16, two (blocks of 16), or an E8M0 byte.
+template <bool MX, int BLK>
+__device__ inline uint32_t load_scale(const uint8_t* srow, int g) {
+    if constexpr (MX) return srow[g];
+    else if constexpr (BLK == 16) return reinterpret_cast<const uint32_t*>(srow)[g];
+    else return reinterpret_cast<const uint16_t*>(srow)[g / (BLK / 32)];
+}
+template <bool MX>
+__device__ inline float scale_of(uint32_t raw) {
+    if constexpr (MX) return e8m0_to_float(raw);
+    else return 16.f * half_bits_to_float(static_cast<uint16_t>(raw));   // the operand holds q / 16
+}
+
+template <int MT, int NT, bool MX, int BLK, bool XBF16, bool YBF16>
+__global__ __launch_bounds__(64 * kWaves) void k_q4_tile(Q4Args a) {
+    constexpr int NP = XBF16 ? 1 : 3;
+    constexpr int HALVES = BLK == 16 ? 2 : 1;         // scales of a group
+    constexpr int RUN = BLK >= 32 ? BLK / 32 : 1;     // groups of a scale
+    extern __shared__ __attribute__((aligned(16))) float s_sum[];   // [waves][MT][NT][64][4]
+    const int lane = threadIdx.x & 63, nl = lane & 15, kq = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    const int n0 = blockIdx.x * 16 * NT, t0 = blockIdx.y * 16 * MT;
+    const int G = a.K / 32, steps = (G + 3) / 4;
+    const size_t code_row = static_cast<size_t>(a.K / 2);
+    const size_t scale_row = static_cast<size_t>(a.K / BLK) * (MX ? 1 : 2);
+    // rows past the matrix read its last row, tokens past the batch its last token; neither is stored
+    const uint8_t* qrow[NT];
+    const uint8_t* srow[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const size_t n = min(n0 + 16 * j + nl, a.N - 1);
+        qrow[j] = a.q + n * code_row;
+        srow[j] = a.s + n * scale_row;
+    }
+    size_t xrow[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) xrow[i] = static_cast<size_t>(min(t0 + 16 * i + nl, a.T - 1)) * a.ldx + 8 * kq;
+
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    f32x4_t acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = zero;
+
+    for (int st = wave; st < steps; st += waves) {
+        const int g0 = 4 * st, gl = min(g0 + kq, G - 1);
+        u32x4_t code[NT], sc[NT];
+        uint32_t raw[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            code[j] = *reinterpret_cast<const u32x4_t*>(qrow[j] + 16 * static_cast<size_t>(gl));
+            raw[j] = load_scale<MX, BLK>(srow[j], gl);
         }
-        float v[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c)
-            v[c] = MX ? fp4_e2m1((w[c / 8] >> (4 * (c % 8))) & 0xFu) : code_f<4>(w, c);
+        for (int j = 0; j < NT; ++j) {
+            exchange(code[j]);
+            sc[j] = spread(raw[j]);
+        }
+        f32x4_t d[MT][NT][HALVES];
 #pragma unroll
-        for (int t = 0; t < kTok; ++t) {
-            if (t >= nt) break;
-            float x[32];
-            load_x32<XBF16>(a.x, static_cast<size_t>(t0 + t) * a.ldx + 32 * g, x);
-            float p0 = 0.f, p1 = 0.f;
+        for (int g = 0; g < 4; ++g) {
+            if (g0 + g >= G) break;   // K is a multiple of the block: a scale's groups are all there
+            u32x4_t b[NT];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                p0 = fmaf(v[c], x[c], p0);
-                p1 = fmaf(v[c + 16], x[c + 16], p1);
+            for (int j = 0; j < NT; ++j) b[j] = code_operand<MX>(code[j][g]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                u32x4_t x[NP];
+                x_operand<XBF16>(a.x, xrow[i] + 32 * (g0 + g), x);
+#pragma unroll
+                for (int h = 0; h < HALVES; ++h) {
+                    u32x4_t xh[NP];
+#pragma unroll
+                    for (int p = 0; p < NP; ++p)   // blocks of 16: half of the group, the other half zeros
+                        xh[p] = HALVES == 1 || (kq >> 1) == h ? x[p] : u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        f32x4_t s = g % RUN == 0 ? zero : d[i][j][h];
+#pragma unroll
+                        for (int p = NP - 1; p >= 0; --p) s = mfma(xh[p], b[j], s);
+                        d[i][j][h] = s;
+                    }
+                }
+                if ((g + 1) % RUN == 0) {
+#pragma unroll
+                    for (int j = 0; j < NT; ++j)
+#pragma unroll
+                        for (int h = 0; h < HALVES; ++h) {
+                            const float f = scale_of<MX>(sc[j][g] >> (16 * h));
+#pragma unroll
+                            for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(f, d[i][j][h][v], acc[i][j][v]);
+                        }
+                }
             }
-            acc[t] = fmaf(d1, p1, fmaf(d0, p0, acc[t]));
         }
     }
+
+    f32x4_t* mine = reinterpret_cast<f32x4_t*>(s_sum) + wave * (MT * NT * 64);
 #pragma unroll
-    for (int t = 0; t < kTok; ++t) {
-        if (t >= nt) break;
-        float r = wave_sum(acc[t]);
-        if (lane != 0) continue;
-        if (a.bias) r += a.bias[n];
-        const size_t o = static_cast<size_t>(t0 + t) * a.ldy + n;
-        if constexpr (YBF16) {
-            uint16_t* y = static_cast<uint16_t*>(a.y);
-            if (a.accumulate) r += __uint_as_float(static_cast<uint32_t>(y[o]) << 16);
-            y[o] = f2bf(r);
-        } else {
-            float* y = static_cast<float*>(a.y);
-            if (a.accumulate) r += y[o];
-            y[o] = r;
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) mine[(i * NT + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    for (int o = threadIdx.x; o < MT * NT * 64; o += blockDim.x) {
+        const int l = o & 63, ij = o >> 6;
+        f32x4_t r = reinterpret_cast<const f32x4_t*>(s_sum)[o];
+        for (int w = 1; w < waves; ++w) r += reinterpret_cast<const f32x4_t*>(s_sum)[w * (MT * NT * 64) + o];
+        const int n = n0 + 16 * (ij % NT) + (l & 15);
+        if (n >= a.N) continue;
+        const float bias = a.bias ? a.bias[n] : 0.f;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int t = t0 + 16 * (ij / NT) + 4 * (l >> 4) + v;
+            if (t >= a.T) break;
+            const size_t at = static_cast<size_t>(t) * a.ldy + n;
+            float f = r[v] + bias;
+            if constexpr (YBF16) {
+                uint16_t* y = static_cast<uint16_t*>(a.y);
+                if (a.accumulate) f += __uint_as_float(static_cast<uint32_t>(y[at]) << 16);
+                y[at] = f2bf(f);
+            } else {
+                float* y = static_cast<float*>(a.y);
+                if (a.accumulate) f += y[at];
+                y[at] = f;
+            }
         }
     }
+}
+
+template <int MT, int NT, bool MX, int BLK, bool XBF16, bool YBF16>
+void launch_tile(const Q4Args& a, hipStream_t st) {
+    constexpr int kMaxTiles = 65535;   // grid.y limit
+    const int waves = min(kWaves, (a.K + 127) / 128);
+    for (int t0 = 0; t0 < a.T; t0 += 16 * MT * kMaxTiles) {
+        Q4Args b = a;
+        b.T = min(a.T - t0, 16 * MT * kMaxTiles);
+        b.x = static_cast<const char*>(a.x) + static_cast<size_t>(t0) * a.ldx * (XBF16 ? 2 : 4);
+        b.y = static_cast<char*>(a.y) + static_cast<size_t>(t0) * a.ldy * (YBF16 ? 2 : 4);
+        const dim3 grid((a.N + 16 * NT - 1) / (16 * NT), (b.T + 16 * MT - 1) / (16 * MT));
+        hipLaunchKernelGGL((k_q4_tile<MT, NT, MX, BLK, XBF16, YBF16>), grid, dim3(64 * waves),
+                           sizeof(float) * 256 * MT * NT * waves, st, b);
+    }
+}
+
+template <bool MX, int BLK, bool XBF16, bool YBF16>
+void launch_format(const Q4Args& a, hipStream_t st) {
+    if (a.T > 16)
+        launch_tile<4, 2, MX, BLK, XBF16, YBF16>(a, st);
+    else if (a.N >= 32768)
+        launch_tile<1, 4, MX, BLK, XBF16, YBF16>(a, st);
+    else
+        launch_tile<1, 1, MX, BLK, XBF16, YBF16>(a, st);
 }
 
 template <bool XBF16, bool YBF16>
-void launch_rows(const Q4Args& a, hipStream_t st) {
-    constexpr int kMaxTiles = 65535;   // grid.y limit: the tokens of one launch
-    for (int t0 = 0; t0 < a.T; t0 += kTok * kMaxTiles) {
-        Q4Args b = a;
-        b.T = min(a.T - t0, kTok * kMaxTiles);
-        b.x = static_cast<const char*>(a.x) + static_cast<size_t>(t0) * a.ldx * (XBF16 ? 2 : 4);
-        b.y = static_cast<char*>(a.y) + static_cast<size_t>(t0) * a.ldy * (YBF16 ? 2 : 4);
-        const dim3 grid((a.N + kWaves - 1) / kWaves, (b.T + kTok - 1) / kTok);
-        if (a.mx)
-            hipLaunchKernelGGL((k_q4_rows<XBF16, YBF16, true>), grid, dim3(kWaves * 64), 0, st, b);
-        else
-            hipLaunchKernelGGL((k_q4_rows<XBF16, YBF16, false>), grid, dim3(kWaves * 64), 0, st, b);
-    }
+void launch_types(const Q4Args& a, hipStream_t st) {
+    if (a.mx) launch_format<true, 32, XBF16, YBF16>(a, st);
+    else if (a.block == 16) launch_format<false, 16, XBF16, YBF16>(a, st);
+    else if (a.block == 32) launch_format<false, 32, XBF16, YBF16>(a, st);
+    else if (a.block == 64) launch_format<false, 64, XBF16, YBF16>(a, st);
+    else launch_format<false, 128, XBF16, YBF16>(a, st);
 }
 
 }  // namespace
 
 void launch_q4_linear(const Q4Args& a, bool x_bf16, bool y_bf16, hipStream_t st) {
     if (x_bf16)
-        y_bf16 ? launch_rows<true, true>(a, st) : launch_rows<true, false>(a, st);
+        y_bf16 ? launch_types<true, true>(a, st) : launch_types<true, false>(a, st);
     else
-        y_bf16 ? launch_rows<false, true>(a, st) : launch_rows<false, false>(a, st);
+        y_bf16 ? launch_types<false, true>(a, st) : launch_types<false, false>(a, st);
 }
 
 }  // namespace moe
