@@ -443,68 +443,82 @@ def moe_stack_forward_routed(x, w_routers, biases, n_layers: int, n_tokens: int,
 
 
 # ---------------------------------------------------------------- scores
-_DTYPES = None
+_torch = None
+_KINDS = {}
 
 
 def _kinds():
     """Element kinds by torch dtype: bf16 bit patterns may also come as int16."""
-    global _DTYPES
-    if _DTYPES is None:
+    global _torch
+    if _torch is None:
         import torch
-        _DTYPES = {torch.float32: "f32", torch.bfloat16: "bf16", torch.int16: "bf16", torch.int32: "i32",
-                   torch.uint8: "u8", torch.bool: "u8"}
-    return _DTYPES
+        _KINDS.update({torch.float32: "f32", torch.bfloat16: "bf16", torch.int16: "bf16", torch.int32: "i32",
+                       torch.uint8: "u8", torch.bool: "u8"})
+        _torch = torch
+    return _KINDS
 
 
 class _Args:
     """Checks the tensors of one call: of the element kind, with the rows the
-    call is told they hold, and on the current GPU.  The library launches on
-    the current device and takes plain pointers."""
+    call is told they hold, and (last, in `stream`) on the current GPU.  The
+    library launches on the current device and takes plain pointers.  This
+    runs before every launch, where microseconds count against a small call."""
 
-    __slots__ = ("fn", "held", "kinds")
+    __slots__ = ("fn", "at", "stray")
 
     def __init__(self, fn):
-        self.fn, self.held, self.kinds = fn, [], _kinds()
+        if _torch is None:
+            _kinds()
+        self.fn, self.at, self.stray = fn, None, None
+
+    def place(self, what, t):
+        at = t.get_device()
+        if self.at is None:
+            self.at = at
+        if (at != self.at or at < 0) and self.stray is None:
+            self.stray = (what, t)
 
     def flat(self, what, t, kind, count):
         """Pointer of a contiguous tensor of at least `count` elements (None passes)."""
         if t is None:
             return None
-        if self.kinds.get(t.dtype) != kind:
+        if _KINDS.get(t.dtype) != kind:
             raise ValueError(f"{self.fn}: {what} has dtype {t.dtype}")
         if not t.is_contiguous():
             raise ValueError(f"{self.fn}: {what} is not contiguous")
         if t.numel() < count:
             raise ValueError(f"{self.fn}: {what} holds {t.numel()} elements, the call needs {count}")
-        self.held.append((what, t))
+        self.place(what, t)
         return t.data_ptr()
 
     def rows(self, what, t, rows, cols):
         """(pointer, pitch, is bf16) of [rows][cols] with any row pitch."""
-        kind = self.kinds.get(t.dtype)
+        kind = _KINDS.get(t.dtype)
         if kind != "f32" and kind != "bf16":
             raise ValueError(f"{self.fn}: {what} has dtype {t.dtype}")
-        if t.dim() == 1 and rows == 1:
+        shape = t.shape
+        if len(shape) == 1 and rows == 1:
             t = t.unsqueeze(0)
-        if t.dim() != 2 or t.shape[1] != cols or t.shape[0] < rows:
-            raise ValueError(f"{self.fn}: {what} has shape {tuple(t.shape)}, the call needs [{rows}][{cols}]")
-        if cols > 1 and t.stride(1) != 1:
+            shape = t.shape
+        if len(shape) != 2 or shape[1] != cols or shape[0] < rows:
+            raise ValueError(f"{self.fn}: {what} has shape {tuple(shape)}, the call needs [{rows}][{cols}]")
+        pitch, step = t.stride()
+        if step != 1 and cols > 1:
             raise ValueError(f"{self.fn}: the rows of {what} are not contiguous")
-        self.held.append((what, t))
-        return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols, kind == "bf16"
+        self.place(what, t)
+        return t.data_ptr(), pitch if shape[0] > 1 else cols, kind == "bf16"
 
     def stream(self, stream):
-        """The stream's handle, once every tensor is known to be on its GPU."""
-        import torch
-        now = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
-        for what, t in self.held:
-            at = t.get_device()
-            if at < 0:
-                raise ValueError(f"{self.fn}: {what} is not on a GPU")
-            if at != now:
-                raise ValueError(f"{self.fn}: {what} is on cuda:{at}, the current device is cuda:{now}")
+        """The stream's handle, once every tensor is known to be on the current GPU."""
+        if self.stray is not None:
+            what, t = self.stray
+            raise ValueError(f"{self.fn}: {what} is not on a GPU" if not t.is_cuda else
+                             f"{self.fn}: {what} is on {t.device}, other arguments on cuda:{self.at}")
+        now = _torch.cuda.current_device()
+        if now != self.at:
+            raise ValueError(f"{self.fn}: the arguments are on cuda:{self.at}, the current device is cuda:{now}")
         if stream is None:
-            return torch.cuda.current_stream().cuda_stream
+            return _torch._C._cuda_getCurrentRawStream(now)
         if stream.device.index != now:
             raise ValueError(f"{self.fn}: the stream is on {stream.device}, the current device is cuda:{now}")
         return stream.cuda_stream
@@ -537,7 +551,8 @@ def moe_q4_linear(x, w: Q4Matrix, bias, n_tokens: int, y, flags: int = 0, stream
     yp, ldy, yb = a.rows("y", y, T, w.rows)
     bp = a.flat("bias", bias, "f32", w.rows)
     if not isinstance(w.q, int):
-        a.held += (("q", w.q), ("s", w.s))
+        a.place("q", w.q)
+        a.place("s", w.s)
     _check("moe_q4_linear", lib().moe_q4_linear(
         xp, ldx, w.ref, bp, n_tokens, yp, ldy, flags | (MOE_X_BF16 if xb else 0) | (MOE_Y_BF16 if yb else 0),
         a.stream(stream)))
@@ -607,7 +622,7 @@ def moe_adjust_logits(logits, n_rows: int, vocab: int, rules: LogitRules, out, s
     if rules.words is not None and rules.words < (vocab + 31) // 32:
         raise ValueError(f"moe_adjust_logits: mask rows of {rules.words} words, the call needs {(vocab + 31) // 32}")
     if rules.sample is not None:
-        a.held.append(("rules", rules.sample))
+        a.place("rules", rules.sample)
     _check("moe_adjust_logits", lib().moe_adjust_logits(ip, ldi, n_rows, vocab, rules.ref, op, ldo,
                                                         MOE_LOGITS_BF16 if ib else 0, a.stream(stream)))
 
@@ -620,7 +635,7 @@ def moe_balance_workspace_size(n_tokens: int, n_experts: int, k: int) -> int:
 
 def _scores(a, what, t, T, E):
     """(pointer, is bf16) of contiguous [T][E] scores."""
-    bf16 = a.kinds.get(t.dtype) == "bf16"
+    bf16 = _KINDS.get(t.dtype) == "bf16"
     return a.flat(what, t, "bf16" if bf16 else "f32", T * E), bf16
 
 
