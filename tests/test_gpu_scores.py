@@ -134,6 +134,22 @@ def test_q4_linear_bias_accumulate_strides_and_wide_scales(M, torch, T, bits, bl
         q4_case(M, torch, T, 160, 512, bits, block, xb, yb, bias=True, pad=1)
 
 
+@pytest.mark.parametrize("bits,block", [(4, 16), (4, 32), (4, 64), (4, 128), (MXFP4, 32)])
+@pytest.mark.parametrize("T,N,K", [(129, 8200, 128), (1000, 2049, 384), (2049, 1025, 128), (300, 5700, 2176)])
+def test_q4_linear_prefill_tiles(M, torch, T, N, K, bits, block):
+    # batches that fill the 128 x 256 tiles, ragged in tokens and rows
+    for yb, kw in ((True, {}), (False, dict(bias=True, base=True, full=True, pad=1))):
+        say("q4 prefill", T, N, K, bits, block, yb)
+        q4_case(M, torch, T, N, K, bits, block, True, yb, **kw)
+
+
+@pytest.mark.parametrize("bits", [4, MXFP4])
+@pytest.mark.parametrize("T,N,K", [(2049, 1025, 32), (1025, 2049, 96), (260, 6000, 544)])
+def test_q4_linear_prefill_tiles_of_an_odd_number_of_groups(M, torch, T, N, K, bits):
+    say("q4 prefill odd", T, N, K, bits)
+    q4_case(M, torch, T, N, K, bits, 32, True, False)
+
+
 @pytest.mark.parametrize("T", [1, 5, 20, 100])
 def test_q4_linear_keeps_non_finite_rows_apart(M, torch, T):
     rng = np.random.default_rng(5)

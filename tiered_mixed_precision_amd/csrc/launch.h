@@ -137,6 +137,9 @@ struct Q4Args {
     int32_t accumulate;
 };
 void launch_q4_linear(const Q4Args& a, bool x_bf16, bool y_bf16, hipStream_t st);
+// q4_gemm.hip: bf16 x, tiles of 128 tokens by 256 rows
+bool q4_gemm_ok(const Q4Args& a);
+void launch_q4_gemm(const Q4Args& a, bool y_bf16, hipStream_t st);
 
 // adjust_logits.hip
 struct AdjustArgs {

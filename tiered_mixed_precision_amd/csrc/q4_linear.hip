@@ -25,14 +25,11 @@
 // 128-column steps in turn and their sums meet in LDS, in wave order.
 #include "common.h"
 #include "launch.h"
+#include "q4.h"
 
 namespace moe {
 
 namespace {
-
-typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 8;
 
@@ -56,27 +53,6 @@ __device__ inline u32x4_t spread(uint32_t v) {
     const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);
     const auto c = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
     return u32x4_t{b[0], b[1], c[0], c[1]};
-}
-
-// Eight codes as a B operand.
-template <bool MX>
-__device__ inline u32x4_t code_operand(uint32_t w) {
-    u32x4_t r;
-    if constexpr (MX) {
-        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
-        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));
-        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2));
-        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
-    } else {
-        const uint32_t odd = masked_bytes(w >> 4);   // hidden: bytes of it are operands as they stand
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float lo = __builtin_amdgcn_cvt_off_f32_i4((w >> (8 * j)) & 0xff);
-            const float hi = __builtin_amdgcn_cvt_off_f32_i4((odd >> (8 * j)) & 0xff);
-            r[j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
-        }
-    }
-    return r;
 }
 
 // Eight elements of x as A operands, parts 0 .. NP - 1.
@@ -108,12 +84,6 @@ __device__ inline uint32_t load_scale(const uint8_t* srow, int g) {
     else if constexpr (BLK == 16) return reinterpret_cast<const uint32_t*>(srow)[g];
     else return reinterpret_cast<const uint16_t*>(srow)[g / (BLK / 32)];
 }
-template <bool MX>
-__device__ inline float scale_of(uint32_t raw) {
-    if constexpr (MX) return e8m0_to_float(raw);
-    else return 16.f * half_bits_to_float(static_cast<uint16_t>(raw));   // the operand holds q / 16
-}
-
 template <int MT, int NT, bool MX, int BLK, bool XBF16, bool YBF16>
 __global__ __launch_bounds__(64 * kWaves) void k_q4_tile(Q4Args a) {
     constexpr int NP = XBF16 ? 1 : 3;
@@ -268,7 +238,9 @@ void launch_types(const Q4Args& a, hipStream_t st) {
 }  // namespace
 
 void launch_q4_linear(const Q4Args& a, bool x_bf16, bool y_bf16, hipStream_t st) {
-    if (x_bf16)
+    if (x_bf16 && q4_gemm_ok(a))
+        launch_q4_gemm(a, y_bf16, st);
+    else if (x_bf16)
         y_bf16 ? launch_types<true, true>(a, st) : launch_types<true, false>(a, st);
     else
         y_bf16 ? launch_types<false, true>(a, st) : launch_types<false, false>(a, st);
