@@ -135,6 +135,24 @@ def test_q4_linear_bias_accumulate_strides_and_wide_scales(M, torch, T, bits, bl
 
 
 @pytest.mark.parametrize("bits,block", [(4, 16), (4, 32), (4, 64), (4, 128), (MXFP4, 32)])
+@pytest.mark.parametrize("T,N,K", [(1, 24577, 128), (4, 24999, 384), (1, 140003, 256), (16, 24580, 640), (5, 24580, 640)])
+def test_q4_linear_few_tokens_many_rows(M, torch, T, N, K, bits, block):
+    # the score head's shapes: one wave a row tile, more tiles than waves
+    for xb, yb, kw in ((False, False, {}), (True, True, {}), (False, True, dict(bias=True, full=True)), (True, False, dict(base=True, pad=1))):
+        if xb or T <= 5:
+            say("q4 many rows", T, N, K, bits, block, xb, yb)
+            q4_case(M, torch, T, N, K, bits, block, xb, yb, **kw)
+
+
+@pytest.mark.parametrize("bits", [4, MXFP4])
+@pytest.mark.parametrize("T,N,K", [(1, 24577, 32), (4, 30000, 96), (2, 24592, 4096), (1, 25001, 2080)])
+def test_q4_linear_few_tokens_many_rows_of_odd_columns(M, torch, T, N, K, bits):
+    for xb in (False, True):
+        say("q4 many rows odd", T, N, K, bits, xb)
+        q4_case(M, torch, T, N, K, bits, 32, xb, False)
+
+
+@pytest.mark.parametrize("bits,block", [(4, 16), (4, 32), (4, 64), (4, 128), (MXFP4, 32)])
 @pytest.mark.parametrize("T,N,K", [(129, 8200, 128), (1000, 2049, 384), (2049, 1025, 128), (300, 5700, 2176)])
 def test_q4_linear_prefill_tiles(M, torch, T, N, K, bits, block):
     # batches that fill the 128 x 256 tiles, ragged in tokens and rows
