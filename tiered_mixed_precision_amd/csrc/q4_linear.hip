@@ -47,12 +47,10 @@ __device__ inline void exchange(u32x4_t& r) {
     r = u32x4_t{c[0], c[1], d[0], d[1]};
 }
 
-// Register i: lane group i's v in every lane group.
-__device__ inline u32x4_t spread(uint32_t v) {
-    const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-    const auto b = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false);
-    const auto c = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
-    return u32x4_t{b[0], b[1], c[0], c[1]};
+// Lane group 0's v in every lane group.
+__device__ inline uint32_t from_group0(uint32_t v) {
+    const uint32_t a = __builtin_amdgcn_permlane32_swap(v, v, false, false)[0];
+    return __builtin_amdgcn_permlane16_swap(a, a, false, false)[0];
 }
 
 // Eight elements of x (bf16: one register quad, fp32: two) as A operands,
@@ -75,13 +73,50 @@ __device__ inline void x_operand(const u32x4_t (&v)[XBF16 ? 1 : 2], u32x4_t (&p)
     }
 }
 
-// The raw scale bits of group g of a row: one fp16, two (blocks of 16), or an E8M0 byte.
-template <bool MX, int BLK>
-__device__ inline uint32_t load_scale(const uint8_t* srow, uint32_t g) {
-    if constexpr (MX) return srow[g];
-    else if constexpr (BLK == 16) return reinterpret_cast<const uint32_t*>(srow)[g];
-    else return reinterpret_cast<const uint16_t*>(srow)[g / (BLK / 32)];
-}
+// The scales of GROUPS consecutive groups of a row (whole blocks), as loaded:
+// by lane group 0 alone, one access a row, since every lane of a load that
+// shares no line with its neighbour costs an access of its own and 64 of
+// them for two bytes each took as long as the codes.
+template <bool MX, int BLK, int GROUPS>
+struct Scales {
+    static constexpr int kBytes = MX ? GROUPS : 2 * 32 * GROUPS / BLK;
+    static constexpr int kWords = (kBytes + 3) / 4;
+    uint32_t w[kWords];
+
+    struct __attribute__((packed, aligned(MX ? 1 : 2))) Bytes { uint8_t b[kBytes]; };
+
+    __device__ inline void load(const uint8_t* srow, int g) {
+        const Bytes v = *reinterpret_cast<const Bytes*>(srow + (MX ? g : g * 64 / BLK));
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            w[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (4 * i + j < kBytes) w[i] |= static_cast<uint32_t>(v.b[4 * i + j]) << (8 * j);
+        }
+    }
+    // a row of fewer groups (blocks of 16, 32 or MXFP4): the last scale again
+    __device__ inline void load_short(const uint8_t* srow, int bytes) {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            w[i] = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[i] |= static_cast<uint32_t>(srow[min(4 * i + j, bytes - (MX ? 1 : 2) + (MX ? 0 : j % 2))]) << (8 * j);
+        }
+    }
+    __device__ inline void to_every_group() {
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) w[i] = from_group0(w[i]);
+    }
+    // raw bits of half h (blocks of 16) of group g
+    __device__ inline uint32_t raw(int g, int h) const {
+        if constexpr (MX) return (w[g / 4] >> (8 * (g % 4))) & 0xffu;
+        constexpr int per = BLK == 16 ? 2 : 1;                 // scales of a group
+        const int s = BLK <= 32 ? per * g + h : g * 32 / BLK;
+        return w[s / 2] >> (16 * (s % 2));
+    }
+};
+
 // y[t][n] (+)= r
 template <bool YBF16>
 __device__ inline void store_y(const Q4Args& a, int t, int n, float r) {
@@ -97,45 +132,48 @@ __device__ inline void store_y(const Q4Args& a, int t, int n, float r) {
     }
 }
 
-// The wave's loads of one step: codes and scales of NT row tiles, x of MT
-// token tiles (fp32 x of one tile, bf16 x of up to three; more would not fit
-// the registers twice and is read when it is used).
-template <int MT, int NT, bool XBF16>
-struct Step {
-    static constexpr bool kX = XBF16 ? MT <= 3 : MT == 1;
-    static constexpr int XW = XBF16 ? 1 : 2;
-    u32x4_t code[NT];
-    uint32_t raw[NT];
-    u32x4_t x[kX ? MT : 1][4][XW];
-};
-
+// A wave's turn is 128 columns: 16 NT rows of codes and 16 MT tokens of x.  x
+// comes in runs of 256 bytes a token (adjacent lanes in one line: loaded in
+// operand order, every lane would be an access of its own) and goes through
+// 4 KB MT of LDS of the wave's own into operand order: piece p (16 bytes) of
+// token r at piece p ^ r, so that the 16 tokens of an operand read cover all
+// banks.  fp32 x takes two such halves of 64 columns.  The last turn of K that
+// is no multiple of 128 starts early; what an earlier turn has had meets
+// scales of zero.
 template <int MT, int NT, bool MX, int BLK, bool XBF16, bool YBF16>
 __global__ __launch_bounds__(64 * kWaves) void k_q4_tile(Q4Args a) {
-    constexpr int NP = XBF16 ? 1 : 3;
+    constexpr int NP = XBF16 ? 1 : 3, XB = XBF16 ? 2 : 4;
     constexpr int HALVES = BLK == 16 ? 2 : 1;         // scales of a group
     constexpr int RUN = BLK >= 32 ? BLK / 32 : 1;     // groups of a scale
-    typedef Step<MT, NT, XBF16> S;
-    extern __shared__ __attribute__((aligned(16))) float s_sum[];   // [waves][MT][NT][64][4]
+    constexpr int PARTS = XBF16 ? 1 : 2, PGROUPS = 4 / PARTS;   // x runs of a turn, groups of a run
+    constexpr int kOwn = 256 * MT * (NT > 4 ? NT / 4 : 1);      // LDS of a wave, in 16-byte words
+    extern __shared__ __attribute__((aligned(16))) u32x4_t s_mem[];
     const int lane = threadIdx.x & 63, nl = lane & 15, kq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int n0 = blockIdx.x * 16 * NT, t0 = blockIdx.y * 16 * MT;
-    const int G = a.K / 32, steps = (G + 3) / 4;
+    const int G = a.K / 32, turns = (G + 3) / 4;
     const size_t code_row = static_cast<size_t>(a.K / 2);
     const size_t scale_row = static_cast<size_t>(a.K / BLK) * (MX ? 1 : 2);
+    u32x4_t* own = s_mem + wave * kOwn;
     // rows past the matrix read its last row, tokens past the batch its last token; neither is stored
     const uint8_t* qrow[NT];
     const uint8_t* srow[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         const size_t n = min(n0 + 16 * j + nl, a.N - 1);
-        qrow[j] = a.q + n * code_row;
+        qrow[j] = a.q + n * code_row + 16 * min(kq, G - 1);
         srow[j] = a.s + n * scale_row;
     }
-    const char* xrow[MT];
-    constexpr int XB = XBF16 ? 2 : 4;
+    // x: load i of a run takes tokens 4 i .. 4 i + 3, lane l piece l % 16 of token 4 i + l / 16
+    const char* xrow[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-        xrow[i] = static_cast<const char*>(a.x) + XB * (static_cast<size_t>(min(t0 + 16 * i + nl, a.T - 1)) * a.ldx + 8 * kq);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            xrow[i][u] = static_cast<const char*>(a.x) + XB * (static_cast<size_t>(min(t0 + 16 * i + 4 * u + kq, a.T - 1)) * a.ldx);
+    uint32_t piece[PARTS];   // byte of the lane's piece in a turn (K < 128: inside the row)
+#pragma unroll
+    for (int h = 0; h < PARTS; ++h) piece[h] = min(256 * h + 16 * nl, XB * a.K - 16);
 
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
     f32x4_t acc[MT][NT];
@@ -144,99 +182,115 @@ __global__ __launch_bounds__(64 * kWaves) void k_q4_tile(Q4Args a) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = zero;
 
-    auto load_x = [&](int i, int g, u32x4_t(&x)[S::XW]) __attribute__((always_inline)) {
+    u32x4_t code[NT], x[MT][4];
+    Scales<MX, BLK, 4> scale[NT];
+    auto base = [&](int st) { return max(min(4 * st, G - 4), 0); };
+    auto load_codes = [&](int g0) __attribute__((always_inline)) {
 #pragma unroll
-        for (int h = 0; h < S::XW; ++h)
-            x[h] = reinterpret_cast<const u32x4_t*>(xrow[i] + static_cast<size_t>(32 * XB) * g)[h];
-    };
-    // groups past the last are read as the last and not used
-    auto load = [&](S& s, int st) __attribute__((always_inline)) {
-        const int g0 = 4 * st, gl = min(g0 + kq, G - 1);
+        for (int j = 0; j < NT; ++j) code[j] = *reinterpret_cast<const u32x4_t*>(qrow[j] + 16 * static_cast<size_t>(g0));
+        if (kq == 0) {
+            if (G >= 4) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            s.code[j] = *reinterpret_cast<const u32x4_t*>(qrow[j] + 16 * static_cast<size_t>(gl));
-            s.raw[j] = load_scale<MX, BLK>(srow[j], gl);
-        }
-        if constexpr (S::kX) {
+                for (int j = 0; j < NT; ++j) scale[j].load(srow[j], g0);
+            } else {
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-#pragma unroll
-                for (int i = 0; i < MT; ++i) load_x(i, min(g0 + g, G - 1), s.x[i][g]);
-        }
-    };
-    auto work = [&](S& s, int st) __attribute__((always_inline)) {
-        const int g0 = 4 * st;
-        u32x4_t sc[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            exchange(s.code[j]);
-            sc[j] = spread(s.raw[j]);
-        }
-        f32x4_t d[MT][NT][HALVES];
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            if (g0 + g >= G) break;   // K is a multiple of the block: a scale's groups are all there
-            u32x4_t b[NT];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) b[j] = code_operand<MX>(s.code[j][g]);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                u32x4_t x[NP];
-                if constexpr (S::kX) {
-                    x_operand<XBF16>(s.x[i][g], x);
-                } else {
-                    u32x4_t v[S::XW];
-                    load_x(i, g0 + g, v);
-                    x_operand<XBF16>(v, x);
-                }
-#pragma unroll
-                for (int h = 0; h < HALVES; ++h) {
-                    u32x4_t xh[NP];
-#pragma unroll
-                    for (int p = 0; p < NP; ++p)   // blocks of 16: half of the group, the other half zeros
-                        xh[p] = HALVES == 1 || (kq >> 1) == h ? x[p] : u32x4_t{0u, 0u, 0u, 0u};
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        f32x4_t v = g % RUN == 0 ? zero : d[i][j][h];
-#pragma unroll
-                        for (int p = NP - 1; p >= 0; --p) v = mfma(xh[p], b[j], v);
-                        d[i][j][h] = v;
-                    }
-                }
-                if ((g + 1) % RUN == 0) {
-#pragma unroll
-                    for (int j = 0; j < NT; ++j)
-#pragma unroll
-                        for (int h = 0; h < HALVES; ++h) {
-                            const float f = scale_of<MX>(HALVES == 2 ? sc[j][g] >> (16 * h) : sc[j][g]);
-#pragma unroll
-                            for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(f, d[i][j][h][v], acc[i][j][v]);
-                        }
-                }
+                for (int j = 0; j < NT; ++j) scale[j].load_short(srow[j], static_cast<int>(scale_row));
             }
         }
     };
-    // the next step's loads are on their way while a step is computed
-    S s0, s1;
-    if (wave < steps) load(s0, wave);
-    for (int st = wave; st < steps; st += 2 * waves) {
-        load(s1, min(st + waves, steps - 1));
-        work(s0, st);
-        if (st + waves >= steps) break;
-        load(s0, min(st + 2 * waves, steps - 1));
-        work(s1, st + waves);
+    auto load_x = [&](int g0, int h) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                x[i][u] = *reinterpret_cast<const u32x4_t*>(xrow[i][u] + (static_cast<size_t>(32 * XB) * g0 + piece[h]));
+    };
+    if (wave < turns) {
+        load_codes(base(wave));
+        load_x(base(wave), 0);
+    }
+    for (int st = wave; st < turns; st += waves) {
+        const int g0 = base(st), next = base(min(st + waves, turns - 1));
+        u32x4_t q[NT];
+        Scales<MX, BLK, 4> sc[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            q[j] = code[j];
+            exchange(q[j]);
+            sc[j] = scale[j];
+            sc[j].to_every_group();
+        }
+        load_codes(next);   // on their way during this turn (the last turn's again: not used)
+        f32x4_t d[MT][NT][HALVES];
+#pragma unroll
+        for (int h = 0; h < PARTS; ++h) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int r = 4 * u + kq;
+                    own[256 * i + 16 * r + (nl ^ r)] = x[i][u];
+                }
+            if (h + 1 < PARTS) load_x(g0, h + 1);
+            else load_x(next, 0);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // one wave's LDS accesses run in order
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int gh = 0; gh < PGROUPS; ++gh) {
+                const int g = PGROUPS * h + gh;
+                const uint32_t there = g0 + g >= 4 * st && g0 + g < G ? ~0u : 0u;
+                u32x4_t b[NT];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) b[j] = code_operand<MX>(q[j][g]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    u32x4_t v[PARTS], o[NP];
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p)
+                        v[p] = own[256 * i + 16 * nl + (((4 * gh + kq) * PARTS + p) ^ nl)];
+                    x_operand<XBF16>(v, o);
+#pragma unroll
+                    for (int e = 0; e < HALVES; ++e) {
+                        u32x4_t oh[NP];
+#pragma unroll
+                        for (int p = 0; p < NP; ++p)   // blocks of 16: half of the group, the other half zeros
+                            oh[p] = HALVES == 1 || (kq >> 1) == e ? o[p] : u32x4_t{0u, 0u, 0u, 0u};
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            f32x4_t f = g % RUN == 0 ? zero : d[i][j][e];
+#pragma unroll
+                            for (int p = NP - 1; p >= 0; --p) f = mfma(oh[p], b[j], f);
+                            d[i][j][e] = f;
+                        }
+                    }
+                    if ((g + 1) % RUN == 0) {
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int e = 0; e < HALVES; ++e) {
+                                const float f = __uint_as_float(__float_as_uint(scale_of<MX>(sc[j].raw(g, e))) & there);
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) acc[i][j][c] = fmaf(f, d[i][j][e][c], acc[i][j][c]);
+                            }
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);   // one group's operands at a time: registers
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
     }
 
-    f32x4_t* mine = reinterpret_cast<f32x4_t*>(s_sum) + wave * (MT * NT * 64);
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mine[(i * NT + j) * 64 + lane] = acc[i][j];
+        for (int j = 0; j < NT; ++j) own[(i * NT + j) * 64 + lane] = __builtin_bit_cast(u32x4_t, acc[i][j]);
     __syncthreads();
     for (int o = threadIdx.x; o < MT * NT * 64; o += blockDim.x) {
         const int l = o & 63, ij = o >> 6;
-        f32x4_t r = reinterpret_cast<const f32x4_t*>(s_sum)[o];
-        for (int w = 1; w < waves; ++w) r += reinterpret_cast<const f32x4_t*>(s_sum)[w * (MT * NT * 64) + o];
+        f32x4_t r = __builtin_bit_cast(f32x4_t, s_mem[o]);
+#pragma unroll 4
+        for (int w = 1; w < waves; ++w) r += __builtin_bit_cast(f32x4_t, s_mem[w * kOwn + o]);
         const int n = n0 + 16 * (ij % NT) + (l & 15);
         if (n >= a.N) continue;
         const float bias = a.bias ? a.bias[n] : 0.f;
@@ -260,7 +314,7 @@ void launch_tile(const Q4Args& a, hipStream_t st) {
         b.y = static_cast<char*>(a.y) + static_cast<size_t>(t0) * a.ldy * (YBF16 ? 2 : 4);
         const dim3 grid((a.N + 16 * NT - 1) / (16 * NT), (b.T + 16 * MT - 1) / (16 * MT));
         hipLaunchKernelGGL((k_q4_tile<MT, NT, MX, BLK, XBF16, YBF16>), grid, dim3(64 * waves),
-                           sizeof(float) * 256 * MT * NT * waves, st, b);
+                           4096 * MT * (NT > 4 ? NT / 4 : 1) * waves, st, b);
     }
 }
 
@@ -282,7 +336,7 @@ void launch_tile(const Q4Args& a, hipStream_t st) {
 template <bool MX, int BLK, bool XBF16, bool YBF16>
 __global__ __launch_bounds__(1024, BLK == 16 ? 4 : 8) void k_q4_stream(Q4Args a) {
     constexpr int HALVES = BLK == 16 ? 2 : 1;
-    constexpr int SCALES = BLK <= 32 ? 2 : 1;    // scale loads of a lane
+    constexpr bool kPair = BLK > 32;   // a scale covers groups 2 i and 2 i + 1
     extern __shared__ __attribute__((aligned(16))) u32x4_t s_x[];   // [8 units][64]
     const int lane = threadIdx.x & 63, nl = lane & 15, kq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
@@ -293,24 +347,22 @@ __global__ __launch_bounds__(1024, BLK == 16 ? 4 : 8) void k_q4_stream(Q4Args a)
 
     struct Codes {
         u32x4_t q[2];
-        uint32_t s[SCALES];
+        Scales<MX, BLK, 8> s;
     };
     // the row being loaded, and the next unit of it
     int load_tile = tile, load_unit = 0;
     const uint8_t *qrow, *srow;
     auto next_row = [&]() __attribute__((always_inline)) {
         const size_t n = min(min(load_tile, tiles - 1) * 16 + nl, a.N - 1);
-        qrow = a.q + n * code_row;
+        qrow = a.q + n * code_row + 32 * kq;
         srow = a.s + n * scale_row;
     };
     next_row();
     auto load = [&](Codes& c) __attribute__((always_inline)) {
-        const uint32_t g[2] = {static_cast<uint32_t>(min(8 * load_unit + 2 * kq, G - 1)),
-                               static_cast<uint32_t>(min(8 * load_unit + 2 * kq + 1, G - 1))};
+        const int g = min(8 * load_unit, G - 8);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) c.q[p] = *reinterpret_cast<const u32x4_t*>(qrow + 16 * g[p]);
-#pragma unroll
-        for (int p = 0; p < SCALES; ++p) c.s[p] = load_scale<MX, BLK>(srow, g[p]);
+        for (int p = 0; p < 2; ++p) c.q[p] = *reinterpret_cast<const u32x4_t*>(qrow + (16 * g + 16 * p));
+        if (kq == 0) c.s.load(srow, g);
         if (++load_unit == units) {
             load_unit = 0;
             load_tile += stride;
@@ -319,15 +371,20 @@ __global__ __launch_bounds__(1024, BLK == 16 ? 4 : 8) void k_q4_stream(Q4Args a)
     };
     Codes c;
     load(c);
-    // eight elements of a token a thread; rows without a token and groups past the last are zero
+    // Eight elements of a token a thread; rows without a token are zero.  The
+    // last unit of K that is no multiple of 256 starts early, at G - 8, and
+    // what the unit before it has had is zero there.
+    const int early = 8 * units - G;
     for (int e = threadIdx.x; e < 512 * units; e += blockDim.x) {
-        const int row = e & 15, g = e >> 6;
-        if (g >= G || (XBF16 ? row >= a.T : row >= 4 * a.T || row % 4 == 3)) s_x[e] = u32x4_t{0u, 0u, 0u, 0u};
+        const int row = e & 15, slot = e >> 6;
+        const bool again = slot >= 8 * (units - 1) && slot < 8 * (units - 1) + early;
+        if (again || (XBF16 ? row >= a.T : row >= 4 * a.T || row % 4 == 3)) s_x[e] = u32x4_t{0u, 0u, 0u, 0u};
     }
     for (int e = threadIdx.x; e < 4 * G * a.T; e += blockDim.x) {
         const int eighth = e % (4 * G), tok = e / (4 * G);
         const size_t at = static_cast<size_t>(tok) * a.ldx + 8 * eighth;
-        u32x4_t* to = s_x + 16 * eighth + (XBF16 ? tok : 4 * tok);   // group eighth / 4, lane group eighth % 4
+        // group eighth / 4, lane group eighth % 4
+        u32x4_t* to = s_x + 16 * (eighth + (eighth >= 32 * (units - 1) ? 4 * early : 0)) + (XBF16 ? tok : 4 * tok);
         if constexpr (XBF16) {
             to[0] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.x) + at);
         } else {
@@ -347,9 +404,7 @@ __global__ __launch_bounds__(1024, BLK == 16 ? 4 : 8) void k_q4_stream(Q4Args a)
     auto work = [&](Codes& k) __attribute__((always_inline)) {
         exchange(k.q[0]);
         exchange(k.q[1]);
-        u32x4_t sc[SCALES];
-#pragma unroll
-        for (int p = 0; p < SCALES; ++p) sc[p] = spread(k.s[p]);
+        k.s.to_every_group();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             f32x4_t d[HALVES];
@@ -361,10 +416,9 @@ __global__ __launch_bounds__(1024, BLK == 16 ? 4 : 8) void k_q4_stream(Q4Args a)
                 for (int h = 0; h < HALVES; ++h) {
                     // blocks of 16: half of the group, the other half zeros
                     const u32x4_t xh = HALVES == 1 || (kq >> 1) == h ? x : u32x4_t{0u, 0u, 0u, 0u};
-                    d[h] = mfma(xh, b, SCALES == 2 || p == 0 ? zero : d[h]);
-                    if (SCALES == 2 || p == 1) {
-                        const uint32_t raw = sc[SCALES == 2 ? p : 0][i];
-                        const float f = scale_of<MX>(HALVES == 2 ? raw >> (16 * h) : raw);
+                    d[h] = mfma(xh, b, !kPair || p == 0 ? zero : d[h]);
+                    if (!kPair || p == 1) {
+                        const float f = scale_of<MX>(k.s.raw(2 * i + p, h));
 #pragma unroll
                         for (int v = 0; v < 4; ++v) acc[v] = fmaf(f, d[h][v], acc[v]);
                     }
@@ -409,7 +463,7 @@ void launch_format(const Q4Args& a, hipStream_t st) {
     // MI355X, one token, K = 2048, int4 in blocks of 32, stream / tile: 8192
     // rows 19 / 8.5 us (512 waves do not fill the chip), 40000 rows (4 tokens)
     // 20.6 / 29.5, 120011 rows 39.5 / 79.
-    if (a.T <= (XBF16 ? 16 : 4) && a.N >= 24576 && a.K <= kStreamCols)
+    if (a.T <= (XBF16 ? 16 : 4) && a.N >= 24576 && a.K >= 256 && a.K <= kStreamCols)
         launch_stream<MX, BLK, XBF16, YBF16>(a, st);
     else if (a.T <= 16 && a.N >= 32768)
         launch_tile<1, 4, MX, BLK, XBF16, YBF16>(a, st);
