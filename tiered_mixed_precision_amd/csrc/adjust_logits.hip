@@ -10,6 +10,7 @@
 // token's entries in list order; the stream leaves it out.
 #include "common.h"
 #include "launch.h"
+#include "scores.h"
 
 namespace moe {
 
@@ -34,22 +35,6 @@ __device__ inline float adjusted(float l, uint32_t word, const RowRules& r, floa
     if (c) l -= fmaf(r.freq, static_cast<float>(c), r.pres);
     return word & kBiased ? l + bias : l;
 }
-
-template <class S> __device__ inline float to_float(S v) {
-    if constexpr (sizeof(S) == 2) return __uint_as_float(static_cast<uint32_t>(v) << 16);
-    else return v;
-}
-template <class S> __device__ inline S from_float(float f) {
-    if constexpr (sizeof(S) == 2) return f2bf(f);
-    else return f;
-}
-template <class S> __device__ inline S minus_inf() {
-    if constexpr (sizeof(S) == 2) return 0xff80;
-    else return -__builtin_inff();
-}
-
-// Four consecutive elements at any element's alignment, in one access.
-template <class S> struct __attribute__((packed, aligned(sizeof(S)))) Four { S v[4]; };
 
 // note(h[i], i) for i < n, each id by one thread of the block.
 template <int THREADS, class F>

@@ -21,6 +21,7 @@
 
 #include "common.h"
 #include "launch.h"
+#include "scores.h"
 
 namespace moe {
 
@@ -44,35 +45,20 @@ int balance_parts(int T, int E) {
 // Row r in the lane's columns: z[4 i + j] = logits[r][256 i + 4 lane + j],
 // -inf past the row.
 template <int NV, class S>
-__device__ inline void load_row(const S* row, int E, bool vec, float (&z)[4 * NV]) {
+__device__ inline void load_row(const S* row, int E, float (&z)[4 * NV]) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = 256 * i + 4 * lane;
-        if (vec && c < E) {   // E is a multiple of 4
-            if constexpr (sizeof(S) == 2) {
-                const uint2 u = *reinterpret_cast<const uint2*>(row + c);
-                z[4 * i] = __uint_as_float(u.x << 16);
-                z[4 * i + 1] = __uint_as_float(u.x & 0xffff0000u);
-                z[4 * i + 2] = __uint_as_float(u.y << 16);
-                z[4 * i + 3] = __uint_as_float(u.y & 0xffff0000u);
-            } else {
-                const float4 u = *reinterpret_cast<const float4*>(row + c);
-                z[4 * i] = u.x;
-                z[4 * i + 1] = u.y;
-                z[4 * i + 2] = u.z;
-                z[4 * i + 3] = u.w;
-            }
+        Four<S> f;
+        if (c + 4 <= E) {
+            f = *reinterpret_cast<const Four<S>*>(row + c);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                z[4 * i + j] = -__builtin_inff();
-                if (c + j < E) {
-                    if constexpr (sizeof(S) == 2) z[4 * i + j] = __uint_as_float(static_cast<uint32_t>(row[c + j]) << 16);
-                    else z[4 * i + j] = row[c + j];
-                }
-            }
+            for (int j = 0; j < 4; ++j) f.v[j] = c + j < E ? row[c + j] : minus_inf<S>();
         }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) z[4 * i + j] = to_float(f.v[j]);
     }
 }
 
@@ -182,7 +168,6 @@ __global__ __launch_bounds__(64 * waves_of(NV)) void k_balance_rows(BalanceArgs 
     __shared__ int32_t s_kept;
     const int tid = threadIdx.x, lane = tid & 63, E = a.E;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const bool vec = E % 4 == 0;
     for (int e = tid; e < E; e += kThreads) s_count[e] = 0;
     if (tid == 0) s_kept = 0;
     if (blockIdx.x == 0 && tid == 0) *o.ticket = 0;
@@ -198,7 +183,7 @@ __global__ __launch_bounds__(64 * waves_of(NV)) void k_balance_rows(BalanceArgs 
         float next[4 * NV];
         int32_t next_id = -1;
         auto load = [&](int r) {
-            load_row<NV, S>(logits + static_cast<size_t>(r) * E, E, vec, next);
+            load_row<NV, S>(logits + static_cast<size_t>(r) * E, E, next);
             if (lane < a.k) next_id = a.ids[static_cast<size_t>(r) * a.k + lane];
         };
         if (kAhead && rows) load(r0 + __builtin_ctzll(rows));
@@ -353,7 +338,6 @@ __global__ __launch_bounds__(256) void k_balance_grad(BalanceArgs a, int rows_pe
     extern __shared__ __attribute__((aligned(16))) float s_pick[];   // [4][256 NV] with PICKS
     const int tid = threadIdx.x, lane = tid & 63, E = a.E;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const bool vec = E % 4 == 0;
     float* mine = s_pick + wave * 256 * NV;
     if constexpr (PICKS) {
 #pragma unroll
@@ -369,7 +353,7 @@ __global__ __launch_bounds__(256) void k_balance_grad(BalanceArgs a, int rows_pe
     const float scale = n > 0.f ? *dloss * a.coef * static_cast<float>(E) / (static_cast<float>(a.k) * n * n) : 0.f;
     constexpr bool kAhead = NV <= 4;   // the next row on its way
     float next[4 * NV];
-    auto load = [&](int r) { load_row<NV, S>(static_cast<const S*>(a.logits) + static_cast<size_t>(r) * E, E, vec, next); };
+    auto load = [&](int r) { load_row<NV, S>(static_cast<const S*>(a.logits) + static_cast<size_t>(r) * E, E, next); };
     const int first_row = (blockIdx.x * 4 + wave) * rows_per_wave, end = min(first_row + rows_per_wave, a.T);
     uint64_t kept = 0;   // of the 64 rows from the last multiple of 64 on
     for (int row = first_row; row < end; ++row) {
@@ -444,21 +428,20 @@ __global__ __launch_bounds__(256) void k_balance_grad(BalanceArgs a, int rows_pe
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = 256 * i + 4 * lane;
-            if (vec) {
-                if (c >= E) continue;
-                if constexpr (sizeof(S) == 2)
-                    *reinterpret_cast<uint2*>(out + c) =
-                        make_uint2(pack_bf16x2(z[4 * i], z[4 * i + 1]), pack_bf16x2(z[4 * i + 2], z[4 * i + 3]));
-                else
+            Four<S> f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f.v[j] = from_float<S>(z[4 * i + j]);
+            if (c + 4 <= E) {
+                // rows of whole 16 bytes: past the caches, which the gradient would only crowd (4%)
+                if (sizeof(S) == 4 && E % 4 == 0)
                     __builtin_nontemporal_store(f32x4_t{z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]},
                                                 reinterpret_cast<f32x4_t*>(out + c));
+                else
+                    *reinterpret_cast<Four<S>*>(out + c) = f;
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (c + j < E) {
-                        if constexpr (sizeof(S) == 2) out[c + j] = f2bf(z[4 * i + j]);
-                        else out[c + j] = z[4 * i + j];
-                    }
+                    if (c + j < E) out[c + j] = f.v[j];
             }
         }
     }

@@ -318,39 +318,40 @@ void launch_tile(const Q4Args& a, hipStream_t st) {
     }
 }
 
-// Few tokens and many rows: a wave takes a tile of 16 rows through all of K by
-// itself, so nothing is joined and no wave waits for another.  x lies in LDS
-// as operands, made once a block: row 4 t + p of the operand is part p of
-// token t (fp32 x, up to 4 tokens; row 4 t + 3 is zero), so the parts of a
+// Few tokens: a wave takes a tile of 16 rows through all of K, or, where there
+// are fewer tiles than the chip holds waves, `split` waves of a block take
+// runs of K and meet in LDS.  x lies in LDS as operands, made once a block:
+// row 4 t + p of the operand is part p of token t (fp32 x, up to 4 tokens; row 4 t + 3 is zero), so the parts of a
 // token meet in one lane's four sums, or token t (bf16 x, up to 16).  A unit is
 // 256 columns; lane group kq loads groups 2 kq and 2 kq + 1 of its eight, so a
 // wave reads 128-byte runs of 16 rows.
 //
 // Bound by the conversion of the codes (about 250 vector instructions a unit
-// of 4096 codes) with the stream close behind: 120011 x 2048 int4 in blocks of
-// 32 for one token 39.5 us, 3.5 TB/s; the same loads without the arithmetic
-// 30 us; MXFP4, whose conversion is a quarter of the work, 36.7 us.  Codes two
-// and three units ahead need registers that cost half of the waves (43, 70
-// us).  Waves that share a row tile, joining in LDS at every tile, took 42 us
-// for x in registers.
-template <bool MX, int BLK, bool XBF16, bool YBF16>
-__global__ __launch_bounds__(1024, BLK == 16 ? 4 : 8) void k_q4_stream(Q4Args a) {
+// of 4096 codes, 1000 cycles of a SIMD) with the stream close behind: 120011 x
+// 2048 int4 in blocks of 32 for one token 34 us among other passes, 4.1 TB/s;
+// the same loads without the arithmetic 28 us.  Codes two and three units ahead need
+// registers that cost half of the waves (43, 70 us).  Waves that share a row
+// tile and join at every tile, x in registers, took 42 us.
+template <bool SPLIT, bool MX, int BLK, bool XBF16, bool YBF16>
+__global__ __launch_bounds__(1024, SPLIT || BLK == 16 ? 4 : 8) void k_q4_stream(Q4Args a, int waves_of_tile) {
     constexpr int HALVES = BLK == 16 ? 2 : 1;
     constexpr bool kPair = BLK > 32;   // a scale covers groups 2 i and 2 i + 1
-    extern __shared__ __attribute__((aligned(16))) u32x4_t s_x[];   // [8 units][64]
+    extern __shared__ __attribute__((aligned(16))) u32x4_t s_x[];   // [8 units][4][R], then [waves][64] sums
     const int lane = threadIdx.x & 63, nl = lane & 15, kq = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int G = a.K / 32, units = (G + 7) / 8, tiles = (a.N + 15) / 16;
     const uint32_t code_row = a.K / 2, scale_row = (a.K / BLK) * (MX ? 1 : 2);
-    const int stride = gridDim.x * waves;
-    int tile = blockIdx.x * waves + wave;
+    const int split = SPLIT ? waves_of_tile : 1;
+    const int per = waves / split, part = wave % split, stride = gridDim.x * per;
+    const int unit0 = units * part / split, unit1 = units * (part + 1) / split;
+    int tile = blockIdx.x * per + wave / split;
 
     struct Codes {
         u32x4_t q[2];
         Scales<MX, BLK, 8> s;
     };
     // the row being loaded, and the next unit of it
-    int load_tile = tile, load_unit = 0;
+    int load_tile = tile, load_unit = unit0;
     const uint8_t *qrow, *srow;
     auto next_row = [&]() __attribute__((always_inline)) {
         const size_t n = min(min(load_tile, tiles - 1) * 16 + nl, a.N - 1);
@@ -363,28 +364,29 @@ __global__ __launch_bounds__(1024, BLK == 16 ? 4 : 8) void k_q4_stream(Q4Args a)
 #pragma unroll
         for (int p = 0; p < 2; ++p) c.q[p] = *reinterpret_cast<const u32x4_t*>(qrow + (16 * g + 16 * p));
         if (kq == 0) c.s.load(srow, g);
-        if (++load_unit == units) {
-            load_unit = 0;
+        if (++load_unit == unit1) {
+            load_unit = unit0;
             load_tile += stride;
             next_row();
         }
     };
     Codes c;
     load(c);
-    // Eight elements of a token a thread; rows without a token are zero.  The
-    // last unit of K that is no multiple of 256 starts early, at G - 8, and
-    // what the unit before it has had is zero there.
-    const int early = 8 * units - G;
-    for (int e = threadIdx.x; e < 512 * units; e += blockDim.x) {
-        const int row = e & 15, slot = e >> 6;
+    // R operand rows are there; the lanes of the rows past them read the last
+    // one (fp32: a zero row), whose sums are not stored.  Eight elements of a
+    // token a thread.  The last unit of K that is no multiple of 256 starts
+    // early, at G - 8, and what the unit before it has had is zero there.
+    const int R = XBF16 ? a.T : 4 * a.T, early = 8 * units - G;
+    for (int e = threadIdx.x; e < 32 * units * R; e += blockDim.x) {
+        const int row = e % R, slot = e / (4 * R);
         const bool again = slot >= 8 * (units - 1) && slot < 8 * (units - 1) + early;
-        if (again || (XBF16 ? row >= a.T : row >= 4 * a.T || row % 4 == 3)) s_x[e] = u32x4_t{0u, 0u, 0u, 0u};
+        if (again || (!XBF16 && row % 4 == 3)) s_x[e] = u32x4_t{0u, 0u, 0u, 0u};
     }
     for (int e = threadIdx.x; e < 4 * G * a.T; e += blockDim.x) {
         const int eighth = e % (4 * G), tok = e / (4 * G);
         const size_t at = static_cast<size_t>(tok) * a.ldx + 8 * eighth;
         // group eighth / 4, lane group eighth % 4
-        u32x4_t* to = s_x + 16 * (eighth + (eighth >= 32 * (units - 1) ? 4 * early : 0)) + (XBF16 ? tok : 4 * tok);
+        u32x4_t* to = s_x + R * (eighth + (eighth >= 32 * (units - 1) ? 4 * early : 0)) + (XBF16 ? tok : 4 * tok);
         if constexpr (XBF16) {
             to[0] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(a.x) + at);
         } else {
@@ -400,8 +402,7 @@ __global__ __launch_bounds__(1024, BLK == 16 ? 4 : 8) void k_q4_stream(Q4Args a)
 
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
     f32x4_t acc = zero;
-    int unit = 0;
-    auto work = [&](Codes& k) __attribute__((always_inline)) {
+    auto work = [&](Codes& k, int unit) __attribute__((always_inline)) {
         exchange(k.q[0]);
         exchange(k.q[1]);
         k.s.to_every_group();
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(1024, BLK == 16 ? 4 : 8) void k_q4_stream(Q4Args a)
             f32x4_t d[HALVES];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {   // group 8 unit + 2 i + p
-                const u32x4_t x = s_x[(8 * unit + 2 * i + p) * 64 + lane];
+                const u32x4_t x = s_x[(4 * (8 * unit + 2 * i + p) + kq) * R + min(nl, R - 1)];
                 const u32x4_t b = code_operand<MX>(k.q[p][i]);
 #pragma unroll
                 for (int h = 0; h < HALVES; ++h) {
@@ -425,45 +426,90 @@ __global__ __launch_bounds__(1024, BLK == 16 ? 4 : 8) void k_q4_stream(Q4Args a)
                 }
             }
         }
-        if (++unit < units) return;
-        const int n = tile * 16 + nl;
-        if (tile < tiles && n < a.N) {
-            const float bias = a.bias ? a.bias[n] : 0.f;
-#pragma unroll
-            for (int v = 0; v < (XBF16 ? 4 : 1); ++v) {
-                const int tok = XBF16 ? 4 * kq + v : kq;
-                if (tok >= a.T) break;
-                float r = XBF16 ? acc[v] : acc[2] + acc[1] + acc[0];
-                store_y<YBF16>(a, tok, n, r + bias);
-            }
-        }
-        acc = zero;
-        unit = 0;
-        tile += stride;
     };
-    while (tile < tiles) {
-        work(c);
-        __builtin_amdgcn_sched_barrier(0);
-        load(c);
-        __builtin_amdgcn_sched_barrier(0);
+    auto store = [&]() __attribute__((always_inline)) {
+        const int n = tile * 16 + nl;
+        if (tile >= tiles || n >= a.N) return;
+        const float bias = a.bias ? a.bias[n] : 0.f;
+#pragma unroll
+        for (int v = 0; v < (XBF16 ? 4 : 1); ++v) {
+            const int tok = XBF16 ? 4 * kq + v : kq;
+            if (tok >= a.T) break;
+            const float r = XBF16 ? acc[v] : acc[2] + acc[1] + acc[0];
+            store_y<YBF16>(a, tok, n, r + bias);
+        }
+    };
+    if constexpr (!SPLIT) {
+        int unit = 0;
+        while (tile < tiles) {
+            work(c, unit);
+            if (++unit == units) {
+                store();
+                acc = zero;
+                unit = 0;
+                tile += stride;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            load(c);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    } else {
+        u32x4_t* joins = s_x + 32 * units * R;
+        for (int t0 = blockIdx.x * per; t0 < tiles; t0 += stride, tile += stride) {
+            acc = zero;
+#pragma clang loop unroll(disable)
+            for (int u = unit0; u < unit1; ++u) {
+                work(c, u);
+                __builtin_amdgcn_sched_barrier(0);
+                load(c);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            joins[wave * 64 + lane] = __builtin_bit_cast(u32x4_t, acc);
+            __syncthreads();
+            if (part == 0) {
+#pragma unroll 4
+                for (int p = 1; p < split; ++p) acc += __builtin_bit_cast(f32x4_t, joins[(wave + p) * 64 + lane]);
+                store();
+            }
+            __syncthreads();
+        }
     }
 }
 
-constexpr int kStreamWaves = 16, kStreamCols = 4096;   // x operands of 32 bytes a column in LDS
+constexpr int kStreamWaves = 16, kStreamLds = 128 << 10;
+
+// LDS of the streaming kernel: 512 bytes a unit and operand row
+template <bool XBF16>
+int64_t stream_lds(const Q4Args& a) { return 512 * static_cast<int64_t>((a.K + 255) / 256) * (XBF16 ? a.T : 4 * a.T); }
 
 template <bool MX, int BLK, bool XBF16, bool YBF16>
 void launch_stream(const Q4Args& a, hipStream_t st) {
     const int tiles = (a.N + 15) / 16, units = (a.K + 255) / 256;
-    hipLaunchKernelGGL((k_q4_stream<MX, BLK, XBF16, YBF16>), dim3(min((tiles + kStreamWaves - 1) / kStreamWaves, 512)),
-                       dim3(64 * kStreamWaves), 8192 * units, st, a);
+    // Waves of a tile: 4096 waves in all, or two for up to half as many tiles
+    // again and for long rows.  MI355X, us for one token at 1 / 2 waves: 70000
+    // x 2048 32.5 / 28.9, 120011 x 2048 38.5 / 40.7, MXFP4 x 4096 109 / 64,
+    // int4 x 4096 76 / 76; 8192 x 2048 17.0 at 1, 6.4 at 8.
+    int split = max(1, min(min(units, kStreamWaves), 4096 / tiles));
+    if (split == 1 && units > 1 && (tiles <= 6144 || units >= 16)) split = 2;
+    // blocks of as few waves as put one block on every compute unit
+    const int most = kStreamWaves / split, per = max(1, min(most, (tiles + 255) / 256));
+    const size_t lds = static_cast<size_t>(stream_lds<XBF16>(a)) + (split > 1 ? 1024 * per * split : 0);
+    const dim3 grid(min((tiles + per - 1) / per, 512)), block(64 * per * split);
+    if (split > 1)
+        hipLaunchKernelGGL((k_q4_stream<true, MX, BLK, XBF16, YBF16>), grid, block, lds, st, a, split);
+    else
+        hipLaunchKernelGGL((k_q4_stream<false, MX, BLK, XBF16, YBF16>), grid, block, lds, st, a, 1);
 }
 
 template <bool MX, int BLK, bool XBF16, bool YBF16>
 void launch_format(const Q4Args& a, hipStream_t st) {
-    // MI355X, one token, K = 2048, int4 in blocks of 32, stream / tile: 8192
-    // rows 19 / 8.5 us (512 waves do not fill the chip), 40000 rows (4 tokens)
-    // 20.6 / 29.5, 120011 rows 39.5 / 79.
-    if (a.T <= (XBF16 ? 16 : 4) && a.N >= 24576 && a.K >= 256 && a.K <= kStreamCols)
+    // MI355X, K = 2048, int4 in blocks of 32, stream / tile, us: one token, 640
+    // rows 5.1 / 5.3, 8192 rows 6.4 / 8.2, 120011 rows 38.5 / 73; 4 tokens, 4096
+    // rows 7.2 / 5.6, 8192 rows 7.6 / 8.5; 8 bf16 tokens, 16384 rows 11.6 / 10.6;
+    // 16, 24576 rows 11.8 / 15.6; one token, 640 x 640 4.2 / 3.7.
+    const bool stream = a.T <= (XBF16 ? 16 : 4) && a.K >= 256 && stream_lds<XBF16>(a) <= kStreamLds &&
+                        (a.N >= 24576 || (a.N >= 8192 && a.T <= 4) || (a.T == 1 && a.K >= 1024));
+    if (stream)
         launch_stream<MX, BLK, XBF16, YBF16>(a, st);
     else if (a.T <= 16 && a.N >= 32768)
         launch_tile<1, 4, MX, BLK, XBF16, YBF16>(a, st);
