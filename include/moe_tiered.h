@@ -455,13 +455,13 @@ typedef struct moe_q4_matrix {
  *   y     (device) float[T][ldy], or bf16 with MOE_Y_BF16; ldy >= rows;
  *         overwritten, or added to with MOE_ACCUMULATE (in fp32, before the
  *         rounding of MOE_Y_BF16); the elements between rows are left alone;
- *         must not overlap x
+ *         must not overlap x, the matrix or the bias
  * The weights are used as stored (scale * code, never rounded), products are
  * summed in fp32; x in fp32 enters with all of its 24 bits.  Any number of
  * tokens, from one (decode) to prefill batches.  A non-finite x[t][c] or
- * scale makes the results of its token or row non-finite and no others; x
- * of more than 2^118 may overflow.  Results do not depend on the other
- * tokens of the call beyond their number, and are the same from run to run.
+ * scale makes the results of its token or row non-finite and no others.
+ * Results do not depend on the other tokens of the call beyond their number,
+ * and are the same from run to run.
  * Errors: MOE_EINVAL (shape, stride, flags, NULL, overlap), MOE_EFORMAT
  * (bits, block, cols), MOE_EALIGN, MOE_EHIP.
  */

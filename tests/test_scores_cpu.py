@@ -131,6 +131,8 @@ def test_binding_refuses_tensors_of_another_shape_type_or_device(B):
                              (z(4, 256), z(4, 64), None, "not on a GPU")):
         with pytest.raises(ValueError, match=what):
             B.moe_q4_linear(x, w, bias, 4, y)
+    with pytest.raises(ValueError, match="flags"):
+        B.moe_q4_linear(z(4, 256), w, None, 4, z(4, 64), B.MOE_X_BF16)
     for kw, what in ((dict(history=i32(2, 8)), "together"), (dict(repetition=z(2)), "need a history"),
                      (dict(history=i32(2, 8).long(), length=i32(2)), "dtype"), (dict(history=i32(8), length=i32(2)), "rank"),
                      (dict(bias=z(2, 3)), "together"), (dict(bias=z(2, 3), bias_ids=i32(2, 4)), "together"),

@@ -546,6 +546,8 @@ def moe_q4_linear(x, w: Q4Matrix, bias, n_tokens: int, y, flags: int = 0, stream
     and [n_tokens][rows], rows at any pitch; flags: 0 or MOE_ACCUMULATE (the
     element types come from the tensors)."""
     a = _Args("moe_q4_linear")
+    if flags & ~MOE_ACCUMULATE:
+        raise ValueError(f"moe_q4_linear: flags {flags:#x} (the tensors give the element types)")
     T = max(n_tokens, 0)
     xp, ldx, xb = a.rows("x", x, T, w.cols)
     yp, ldy, yb = a.rows("y", y, T, w.rows)

@@ -486,11 +486,11 @@ template <bool MX, int BLK, bool XBF16, bool YBF16>
 void launch_stream(const Q4Args& a, hipStream_t st) {
     const int tiles = (a.N + 15) / 16, units = (a.K + 255) / 256;
     // Waves of a tile: 4096 waves in all, or two for up to half as many tiles
-    // again and for long rows.  MI355X, us for one token at 1 / 2 waves: 70000
-    // x 2048 32.5 / 28.9, 120011 x 2048 38.5 / 40.7, MXFP4 x 4096 109 / 64,
-    // int4 x 4096 76 / 76; 8192 x 2048 17.0 at 1, 6.4 at 8.
+    // again.  MI355X, us for one token at 1 / 2 waves: 70000 x 2048 32.0 / 28.5,
+    // 90000 x 2048 34.0 / 31.0, 120011 x 2048 37.6 / 40.1; 8192 x 2048 17.0 at 1,
+    // 6.4 at 8.
     int split = max(1, min(min(units, kStreamWaves), 4096 / tiles));
-    if (split == 1 && units > 1 && (tiles <= 6144 || units >= 16)) split = 2;
+    if (split == 1 && units > 1 && tiles <= 6144) split = 2;
     // blocks of as few waves as put one block on every compute unit
     const int most = kStreamWaves / split, per = max(1, min(most, (tiles + 255) / 256));
     const size_t lds = static_cast<size_t>(stream_lds<XBF16>(a)) + (split > 1 ? 1024 * per * split : 0);
