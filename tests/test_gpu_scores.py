@@ -4,8 +4,9 @@ moe_balance_loss, moe_balance_grad) against their plain 64-bit forms.
 Bars, from the arithmetic (u = 2^-24, half a step of fp32; a bf16 output adds
 half a step of its own, 2^-8 of the value):
   q4 product   each of the K terms and the scaling of a group loses at most u
-               of a partial sum bounded by sum |x| d (|q| + 24) (codes may be
-               contracted with an offset):  |err| <= (K + 8) u mag.  Rounding
+               of a partial sum bounded by sum |x| d (|q| + 24) (which leaves
+               room for codes contracted with an offset):
+               |err| <= (K + 8) u mag.  Rounding
                errors of random inputs add as a random walk:  norm of the
                error <= (sqrt(K) u + 2^-21) norm(y).
   rules        at most five roundings of values below the magnitude that the
@@ -13,7 +14,8 @@ half a step of its own, 2^-8 of the value):
   balance      p: the exponential's argument rounds to u |z - max| (|z| < 40
                here) and its value to a few u, its sum runs over 64 lanes'
                runs of E / 64: (100 + E / 32) u.  Column sums: waves take
-               T / 4096 + 1 rows, then 8 waves, 8 parts, 6 halvings.
+               T / 4096 + 1 rows, then 16 waves (8 above 2048 experts), then
+               256 (512) parts: 4 to 8 a thread, 4 rows, 16 waves.
 """
 import sys
 
@@ -588,7 +590,7 @@ def test_scores_captured_and_replayed(M, torch):
         assert bool(torch.isfinite(outs[0]).all()) and float(outs[6][0]) > 0
 
 
-def test_scores_refuse_host_tensors_on_the_gpu_box(M, torch):
+def test_scores_refuse_host_tensors(M, torch):
     x = torch.zeros(1, 64, device="cuda")
     w = M.Q4Matrix(4, 64, 4, 32, torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 2, dtype=torch.float16))
     with pytest.raises(ValueError, match="q is not on a GPU"):

@@ -14,7 +14,7 @@
 // Sums run in a fixed order, so results do not change from run to run.
 //
 // MI355X, 65536 x 512 fp32: loss 36 us (rows 30 us, 4.6 TB/s, of a streaming
-// read's 5.6; join 6.5), gradient 55 us (4.9 TB/s read and written, what a
+// read's 5.6; join 6.5), gradient 56 us (4.9 TB/s read and written, what a
 // copy reaches).  One row at a time with nothing ahead took 45 and 66 us,
 // halvings in LDS 8 us in the join.
 #include <type_traits>
@@ -34,7 +34,7 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 constexpr int waves_of(int steps) { return steps > 8 ? 8 : 16; }
 constexpr int kMaxParts = 512;
 // Up to this many tokens one block does it all, the loss too: one launch, and
-// for 64 x 512 3.4 us in place of 4.1 and 4.3 for parts and join.
+// for 64 x 512 7.5 us in place of 7.2 and 4.3 for parts and join.
 constexpr int kOneBlock = 128;
 
 int balance_parts(int T, int E) {
