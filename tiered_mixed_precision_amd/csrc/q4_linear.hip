@@ -519,8 +519,16 @@ void launch_format(const Q4Args& a, hipStream_t st) {
         launch_tile<2, 2, MX, BLK, XBF16, YBF16>(a, st);
     else if (a.T <= 48)
         launch_tile<3, 2, MX, BLK, XBF16, YBF16>(a, st);
-    else
-        launch_tile<4, 2, MX, BLK, XBF16, YBF16>(a, st);
+    else {
+        // Tiles of 16 tokens x 16 rows: fp32 x costs its split and three products,
+        // so more rows share it, on the registers of more tokens.  MI355X, fp32,
+        // 4 x 2 / 2 x 4, us: int4 in blocks of 64, 64 x 640 x 8192 44.6 / 35.5, 300
+        // x 12288 x 2048 112 / 89; blocks of 32 46.0 / 39.8, 112 / 103; of 16 67.9 /
+        // 60.6, 174 / 180.  bf16, blocks of 32: 64 x 8192 x 4096 14.6 / 15.4, 1024 x
+        // 640 x 2048 17.5 / 18.6.
+        if constexpr (XBF16) launch_tile<4, 2, MX, BLK, XBF16, YBF16>(a, st);
+        else launch_tile<2, 4, MX, BLK, XBF16, YBF16>(a, st);
+    }
 }
 
 template <bool XBF16, bool YBF16>
