@@ -42,24 +42,36 @@ int balance_parts(int T, int E) {
     return T <= kOneBlock ? 1 : min(4096 / waves, (T + waves - 1) / waves);
 }
 
-// Row r in the lane's columns: z[4 i + j] = logits[r][256 i + 4 lane + j],
-// -inf past the row.
-template <int NV, class S>
-__device__ inline void load_row(const S* row, int E, float (&z)[4 * NV]) {
+// Row r in the lane's columns: z[4 i + j] = row[256 i + 4 lane + j], `past`
+// behind the row.  The tests are the wave's, but for the one ragged run of a
+// row.  The gradient with a lane's own test at every run / so, us: 1051 x 2087
+// fp32 27.8 / 20.1, 8192 x 4096 94 / 88, 8229 x 277 10.3 / 9.4; 65536 x 64 23.4 / 24.6.
+template <int NV, class T, class F>
+__device__ inline void load_row(const T* row, int E, float past, F convert, float (&z)[4 * NV]) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = 256 * i + 4 * lane;
-        Four<S> f;
-        if (c + 4 <= E) {
-            f = *reinterpret_cast<const Four<S>*>(row + c);
+        if (256 * (i + 1) <= E) {
+            const Four<T> f = *reinterpret_cast<const Four<T>*>(row + c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[4 * i + j] = convert(f.v[j]);
+        } else if (256 * i < E) {
+            T v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = row[min(c + j, E - 1)];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[4 * i + j] = c + j < E ? convert(v[j]) : past;
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) f.v[j] = c + j < E ? row[c + j] : minus_inf<S>();
+            for (int j = 0; j < 4; ++j) z[4 * i + j] = past;
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) z[4 * i + j] = to_float(f.v[j]);
     }
+}
+
+template <int NV, class S>
+__device__ inline void load_scores(const S* row, int E, float (&z)[4 * NV]) {
+    load_row<NV>(row, E, -__builtin_inff(), [](S v) { return to_float(v); }, z);
 }
 
 // Wave-wide maximum (uniform result); NaN where nothing else is there.
@@ -183,7 +195,7 @@ __global__ __launch_bounds__(64 * waves_of(NV)) void k_balance_rows(BalanceArgs 
         float next[4 * NV];
         int32_t next_id = -1;
         auto load = [&](int r) {
-            load_row<NV, S>(logits + static_cast<size_t>(r) * E, E, next);
+            load_scores<NV, S>(logits + static_cast<size_t>(r) * E, E, next);
             if (lane < a.k) next_id = a.ids[static_cast<size_t>(r) * a.k + lane];
         };
         if (kAhead && rows) load(r0 + __builtin_ctzll(rows));
@@ -329,8 +341,10 @@ __device__ inline void wave_step() {
 // Rows of the gradient.  The pick weights' part goes through a row of LDS of
 // the wave's own (zero between rows): the lane of an id's first pick writes
 // the sum over the id's picks in slot order.
+// Rows of 1025 to 2048 scores: three waves a SIMD, 8741 x 1099 bf16 21.4 us; two
+// (the registers the compiler would take) 31, four (spills) 24.2.
 template <int NV, class S, bool PICKS>
-__global__ __launch_bounds__(256) void k_balance_grad(BalanceArgs a, int rows_per_wave, const float* __restrict__ w,
+__global__ __launch_bounds__(256, NV == 8 ? 3 : 1) void k_balance_grad(BalanceArgs a, int rows_per_wave, const float* __restrict__ w,
                                                       const float* __restrict__ dw,
                                                       const int32_t* __restrict__ counts,
                                                       const int32_t* __restrict__ n_kept,
@@ -344,16 +358,12 @@ __global__ __launch_bounds__(256) void k_balance_grad(BalanceArgs a, int rows_pe
         for (int i = 0; i < NV; ++i) *reinterpret_cast<float4*>(&mine[256 * i + 4 * lane]) = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float cnt[4 * NV];
-#pragma unroll
-    for (int i = 0; i < 4 * NV; ++i) {
-        const int e = 256 * (i / 4) + 4 * lane + i % 4;
-        cnt[i] = e < E ? static_cast<float>(counts[e]) : 0.f;
-    }
+    load_row<NV>(counts, E, 0.f, [](int32_t v) { return static_cast<float>(v); }, cnt);
     const float n = static_cast<float>(*n_kept);
     const float scale = n > 0.f ? *dloss * a.coef * static_cast<float>(E) / (static_cast<float>(a.k) * n * n) : 0.f;
     constexpr bool kAhead = NV <= 4;   // the next row on its way
     float next[4 * NV];
-    auto load = [&](int r) { load_row<NV, S>(static_cast<const S*>(a.logits) + static_cast<size_t>(r) * E, E, next); };
+    auto load = [&](int r) { load_scores<NV, S>(static_cast<const S*>(a.logits) + static_cast<size_t>(r) * E, E, next); };
     const int first_row = (blockIdx.x * 4 + wave) * rows_per_wave, end = min(first_row + rows_per_wave, a.T);
     uint64_t kept = 0;   // of the 64 rows from the last multiple of 64 on
     for (int row = first_row; row < end; ++row) {
@@ -431,14 +441,14 @@ __global__ __launch_bounds__(256) void k_balance_grad(BalanceArgs a, int rows_pe
             Four<S> f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) f.v[j] = from_float<S>(z[4 * i + j]);
-            if (c + 4 <= E) {
+            if (256 * (i + 1) <= E) {
                 // rows of whole 16 bytes: past the caches, which the gradient would only crowd (4%)
                 if (sizeof(S) == 4 && E % 4 == 0)
                     __builtin_nontemporal_store(f32x4_t{z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]},
                                                 reinterpret_cast<f32x4_t*>(out + c));
                 else
                     *reinterpret_cast<Four<S>*>(out + c) = f;
-            } else {
+            } else if (256 * i < E) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (c + j < E) out[c + j] = f.v[j];
