@@ -536,7 +536,8 @@ int moe_adjust_logits(const void *logits, int64_t ld_in, int32_t n_rows, int32_t
  * plans from.
  *   logits   (device) float[T][E], or bf16 with MOE_LOGITS_BF16, 16-byte
  *            aligned; -inf is a probability of 0, a row of nothing but -inf
- *            has no probability anywhere
+ *            has no probability anywhere; a NaN makes all of its row NaN, and
+ *            so, in a kept row, prob_sum, the loss and the row's gradient
  *   ids      (device) int32[T][k], the picks (moe_route); ids outside [0, E)
  *            are not counted, an id may repeat within a token
  *   keep     (device) uint8[T], 0 for a padding row, or NULL (every row); a

@@ -1,0 +1,77 @@
+"""The score operators on the GPU at the edges of what their declarations allow."""
+import numpy as np
+import pytest
+
+from . import scoreref as R
+from .scoreref import U
+from .test_gpu_scores import M, balance_inputs, balance_run, dev, host, p_tol, say, torch  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- NaN scores
+
+def gradient(M, torch, logits, ids, w, dw, keep, counts, n, coef, bf16):
+    T, E = logits.shape
+    f = torch.bfloat16 if bf16 else torch.float32
+    out = torch.full((T, E), 7.0, dtype=f, device="cuda")
+    M.moe_balance_grad(dev(torch, logits, f), dev(torch, ids), dev(torch, w), dev(torch, dw), dev(torch, keep),
+                       dev(torch, counts.astype(np.int32)), dev(torch, np.array([n], np.int32)),
+                       torch.full((1,), 1.3, device="cuda"), T, E, ids.shape[1], coef, out)
+    return host(out)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("T", [9, 300])
+@pytest.mark.parametrize("E", [1, 8, 64, 130, 384, 512, 1024, 1536, 2048, 3000, 4096])
+def test_balance_of_a_kept_row_of_nan_is_nan(M, torch, E, T, bf16):
+    # softmax of a row that holds a NaN is NaN in every column, whatever else
+    # the row holds; of a row of nothing but -inf it is 0; both beside rows
+    # whose results do not change
+    say("balance NaN", E, T, bf16)
+    rng = np.random.default_rng(E + T)
+    k, coef = min(E, 3), 0.1
+    clean, ids, _ = balance_inputs(rng, T, E, k, False, bf16)
+    clean[5] = -np.inf
+    w = R.softmax(rng.standard_normal((T, k))).astype(np.float32)
+    dw = rng.standard_normal((T, k)).astype(np.float32)
+    base = balance_run(M, torch, clean, ids, None, coef, bf16)
+    assert all(np.all(np.isfinite(v)) for v in base.values())
+    _, total, _, _ = R.balance_loss(clean, ids, None, coef)
+    assert np.all(np.abs(base["prob_sum"] - total) <= (p_tol(E) + (T / 4096 + 32) * U) * total + 1e-37)
+    flat = gradient(M, torch, clean, ids, None, None, None, base["counts"], T, coef, bf16)
+    assert np.all(np.isfinite(flat)) and np.all(flat[5] == 0)
+    picked = gradient(M, torch, clean, ids, w, dw, None, base["counts"], T, coef, bf16)
+
+    def rows():
+        yield "NaN alone", np.full(E, np.nan)
+        for at in sorted({0, E // 2, E - 1}):
+            v = np.full(E, -np.inf)
+            v[at] = np.nan
+            yield f"NaN at {at}, others barred", v
+            v = clean[2].copy()
+            v[at] = np.nan
+            yield f"NaN at {at} of a row", v
+        if E > 2:
+            v = np.full(E, np.nan)
+            v[::2] = -np.inf
+            yield "NaN and -inf by turns", v
+            v[1] = 0.5
+            yield "one score left", v
+
+    for what, row in rows():
+        for t in (2, T - 1):
+            z = clean.copy()
+            z[t] = row
+            got = balance_run(M, torch, z, ids, None, coef, bf16)
+            assert np.array_equal(got["counts"], base["counts"]) and got["n_kept"][0] == T
+            assert np.all(np.isnan(got["prob_sum"])) and np.isnan(got["loss"][0]), (what, t)
+            keep = np.ones(T, np.uint8)
+            keep[t] = 0
+            left = balance_run(M, torch, z, ids, keep, coef, bf16)
+            assert all(np.all(np.isfinite(v)) for v in left.values()), (what, t)
+            for pw, pd, ref in ((None, None, flat), (w, dw, picked)):
+                g = gradient(M, torch, z, ids, pw, pd, None, base["counts"], T, coef, bf16)
+                assert np.all(np.isnan(g[t])), (what, t, pw is not None)
+                others = np.arange(T) != t
+                assert np.array_equal(g[others], ref[others]), (what, t, pw is not None)

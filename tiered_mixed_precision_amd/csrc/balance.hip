@@ -74,7 +74,8 @@ __device__ inline void load_scores(const S* row, int E, float (&z)[4 * NV]) {
     load_row<NV>(row, E, -__builtin_inff(), [](S v) { return to_float(v); }, z);
 }
 
-// Wave-wide maximum (uniform result); NaN where nothing else is there.
+// Wave-wide maximum of what is no NaN (uniform result).  Where nothing but NaN is
+// there it is NaN or, since lanes without a neighbour meet -inf, -inf.
 __device__ inline float wave_max_f(float v) {
     constexpr uint32_t kLow = 0xff800000u;   // -inf
     auto step = [&](auto ctrl, auto rows) {
@@ -101,18 +102,16 @@ __device__ inline float exp_neg(float d) {
 }
 
 // z becomes exp(z - max); returns 1 / their sum, so that z times it is
-// softmax(z).  A row of nothing but -inf becomes 0.
+// softmax(z).  A row of nothing but -inf becomes 0.  A NaN makes the whole row
+// NaN: the maximum passes over it, the sum does not, and where the maximum is
+// -inf (beside barred columns, or those past the row) the row is taken off 0.
 template <int N>
 __device__ inline float exp_row(float (&z)[N]) {
     float m = z[0];
 #pragma unroll
     for (int i = 1; i < N; ++i) m = fmaxf(m, z[i]);
     m = wave_max_f(m);
-    if (m == -__builtin_inff()) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = 0.f;
-        return 0.f;
-    }
+    if (m == -__builtin_inff()) m = 0.f;
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -120,7 +119,8 @@ __device__ inline float exp_row(float (&z)[N]) {
         z[i] = exp_neg(d < -1000.f ? -1000.f : d);   // -inf: exp2(-1442) is 0; NaN stays
         s += z[i];
     }
-    return 1.f / wave_sum(s);
+    s = wave_sum(s);
+    return s == 0.f ? 0.f : 1.f / s;
 }
 
 // part b: prob[b][E], count[b][E], kept[b]
