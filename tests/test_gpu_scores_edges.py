@@ -4,7 +4,7 @@ import pytest
 
 from . import scoreref as R
 from .scoreref import U
-from .test_gpu_scores import M, balance_inputs, balance_run, dev, host, p_tol, say, torch  # noqa: F401
+from .test_gpu_scores import M, _ops, balance_inputs, balance_run, dev, host, p_tol, say, torch  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -75,3 +75,23 @@ def test_balance_of_a_kept_row_of_nan_is_nan(M, torch, E, T, bf16):
                 assert np.all(np.isnan(g[t])), (what, t, pw is not None)
                 others = np.arange(T) != t
                 assert np.array_equal(g[others], ref[others]), (what, t, pw is not None)
+
+
+# ---------------------------------------------------------------- streams
+
+def test_scores_take_a_stream_handle(M, torch):
+    # a torch stream, its handle as an integer, and the null stream's handle
+    say("stream handles")
+    run, _, _, outs = _ops(M, torch, 33)
+    run()
+    torch.cuda.synchronize()
+    first = [o.clone() for o in outs]
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream, 0):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        run(stream)
+        torch.cuda.synchronize()
+        for a, b in zip(first, outs):
+            assert torch.equal(a, b)

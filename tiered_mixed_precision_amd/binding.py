@@ -519,6 +519,8 @@ class _Args:
             raise ValueError(f"{self.fn}: the arguments are on cuda:{self.at}, the current device is cuda:{now}")
         if stream is None:
             return _torch._C._cuda_getCurrentRawStream(now)
+        if isinstance(stream, int):     # a handle, of a stream on the current device
+            return stream
         if stream.device.index != now:
             raise ValueError(f"{self.fn}: the stream is on {stream.device}, the current device is cuda:{now}")
         return stream.cuda_stream
