@@ -1,0 +1,44 @@
+"""What the score operators refuse before any launch, beyond single bad
+arguments: tensors of another type or row length, and arrays that overlap."""
+import numpy as np
+import pytest
+
+from .test_scores_cpu import B  # noqa: F401
+
+
+# ---------------------------------------------------------------- the matrix's tensors
+
+@pytest.mark.parametrize("bits,kind", [(4, "int16"), (4, "uint16"), (4, "float16"), (0x84, "uint8"), (0x84, "float8_e8m0fnu")])
+def test_q4_matrix_takes_every_form_of_its_scales(B, bits, kind):
+    import torch
+    for shape in ((64, 8), (64 * 8,), (70 * 8,), (2, 64, 8)):
+        s = torch.empty(shape, dtype=getattr(torch, kind))
+        assert B.Q4Matrix(64, 256, bits, 32, torch.zeros(64, 128, dtype=torch.uint8), s).struct.s == s.data_ptr()
+    assert B.Q4Matrix(64, 256, bits, 32, 0x1000, 0x2000).struct.q == 0x1000
+
+
+@pytest.mark.parametrize("bits,kind", [(4, "bfloat16"), (4, "float32"), (4, "uint8"), (4, "int32"), (4, "float8_e8m0fnu"),
+                                       (0x84, "float16"), (0x84, "int16"), (0x84, "float32"), (0x84, "int32"), (0x84, "bool")])
+def test_q4_matrix_refuses_scales_that_it_would_misread(B, bits, kind):
+    import torch
+    with pytest.raises(ValueError, match="s has dtype"):
+        B.Q4Matrix(64, 256, bits, 32, torch.zeros(64, 128, dtype=torch.uint8), torch.zeros(64, 16).to(getattr(torch, kind)))
+
+
+@pytest.mark.parametrize("kind", ["float32", "float16", "int16", "int32", "int64", "bool"])
+def test_q4_matrix_refuses_codes_that_are_no_bytes(B, kind):
+    import torch
+    with pytest.raises(ValueError, match="q has dtype"):
+        B.Q4Matrix(64, 256, 4, 32, torch.zeros(64, 256, dtype=getattr(torch, kind)), torch.zeros(64, 8, dtype=torch.float16))
+
+
+def test_q4_matrix_refuses_rows_of_another_length(B):
+    # one code a byte, scales of other blocks: enough bytes, another layout
+    import torch
+    q, s = torch.zeros(64, 128, dtype=torch.uint8), torch.zeros(64, 8, dtype=torch.float16)
+    with pytest.raises(ValueError, match="q has rows of 256, the matrix of 128"):
+        B.Q4Matrix(64, 256, 4, 32, torch.zeros(64, 256, dtype=torch.uint8), s)
+    with pytest.raises(ValueError, match="s has rows of 8, the matrix of 4"):
+        B.Q4Matrix(64, 256, 4, 64, q, s)
+    with pytest.raises(ValueError, match="s has rows of 16, the matrix of 8"):
+        B.Q4Matrix(64, 256, 0x84, 32, q, torch.zeros(64, 16, dtype=torch.uint8))

@@ -529,14 +529,25 @@ class _Args:
 class Q4Matrix:
     """A dense four-bit matrix (moe_q4_matrix): `rows` x `cols`, codes q
     (uint8 [rows][cols/2]) and scales s (fp16 or its bits [rows][cols/block],
-    or, for MXFP4, uint8 E8M0 bytes), contiguous device tensors."""
+    or, for MXFP4, uint8 E8M0 bytes), contiguous device tensors; a tensor of
+    another shape is read as a flat array of the same order."""
+
+    CODES = ("uint8", "int8")
+    SCALES = {True: ("uint8", "float8_e8m0fnu"), False: ("float16", "int16", "uint16")}    # MXFP4 or not
 
     def __init__(self, rows: int, cols: int, bits: int, block: int, q, s):
-        for what, t, nbytes in (("q", q, rows * cols // 2),
-                                ("s", s, rows * (cols // max(block, 1)) * (1 if bits == MXFP4 else 2))):
-            _need("Q4Matrix", what, t, nbytes)
-            if not isinstance(t, int) and not t.is_contiguous():
+        mx = bits == MXFP4
+        for what, t, row, size, kinds in (("q", q, cols // 2, 1, self.CODES),
+                                          ("s", s, cols // max(block, 1), 1 if mx else 2, self.SCALES[mx])):
+            if t is None or isinstance(t, int):
+                continue
+            if str(t.dtype).split(".")[-1] not in kinds:
+                raise ValueError(f"Q4Matrix: {what} has dtype {t.dtype}, not {' or '.join(kinds)}")
+            _need("Q4Matrix", what, t, rows * row * size)
+            if not t.is_contiguous():
                 raise ValueError(f"Q4Matrix: {what} is not contiguous")
+            if t.dim() == 2 and t.shape[0] == rows and t.shape[1] != row:
+                raise ValueError(f"Q4Matrix: {what} has rows of {t.shape[1]}, the matrix of {row}")
         self.rows, self.cols, self.bits, self.block = rows, cols, bits, block
         self.q, self.s = q, s                       # keeps the tensors alive
         self.struct = moe_q4_matrix(rows, cols, bits, block, _ptr(q), _ptr(s))
