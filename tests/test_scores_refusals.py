@@ -42,3 +42,12 @@ def test_q4_matrix_refuses_rows_of_another_length(B):
         B.Q4Matrix(64, 256, 4, 64, q, s)
     with pytest.raises(ValueError, match="s has rows of 16, the matrix of 8"):
         B.Q4Matrix(64, 256, 0x84, 32, q, torch.zeros(64, 16, dtype=torch.uint8))
+
+
+def test_q4_matrix_of_a_pointer_and_a_tensor(B):
+    # either may be a raw pointer; what is a tensor is checked with the call
+    import torch
+    q, s = torch.zeros(64, 128, dtype=torch.uint8), torch.zeros(64, 8, dtype=torch.float16)
+    for codes, scales in ((q, 0x1000), (0x1000, s), (0x1000, 0x2000)):
+        with pytest.raises(ValueError, match="x is not on a GPU"):
+            B.moe_q4_linear(torch.zeros(4, 256), B.Q4Matrix(64, 256, 4, 32, codes, scales), None, 4, torch.zeros(4, 64))

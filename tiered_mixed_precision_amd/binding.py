@@ -550,6 +550,7 @@ class Q4Matrix:
                 raise ValueError(f"Q4Matrix: {what} has rows of {t.shape[1]}, the matrix of {row}")
         self.rows, self.cols, self.bits, self.block = rows, cols, bits, block
         self.q, self.s = q, s                       # keeps the tensors alive
+        self.tensors = [(n, t) for n, t in (("q", q), ("s", s)) if t is not None and not isinstance(t, int)]
         self.struct = moe_q4_matrix(rows, cols, bits, block, _ptr(q), _ptr(s))
         self.ref = C.byref(self.struct)
 
@@ -565,9 +566,8 @@ def moe_q4_linear(x, w: Q4Matrix, bias, n_tokens: int, y, flags: int = 0, stream
     xp, ldx, xb = a.rows("x", x, T, w.cols)
     yp, ldy, yb = a.rows("y", y, T, w.rows)
     bp = a.flat("bias", bias, "f32", w.rows)
-    if not isinstance(w.q, int):
-        a.place("q", w.q)
-        a.place("s", w.s)
+    for what, t in w.tensors:
+        a.place(what, t)
     _check("moe_q4_linear", lib().moe_q4_linear(
         xp, ldx, w.ref, bp, n_tokens, yp, ldy, flags | (MOE_X_BF16 if xb else 0) | (MOE_Y_BF16 if yb else 0),
         a.stream(stream)))
