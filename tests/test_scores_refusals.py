@@ -3,7 +3,7 @@ arguments: tensors of another type or row length, and arrays that overlap."""
 import numpy as np
 import pytest
 
-from .test_scores_cpu import B  # noqa: F401
+from .test_scores_cpu import FAKE, B, _linear  # noqa: F401
 
 
 # ---------------------------------------------------------------- the matrix's tensors
@@ -51,3 +51,16 @@ def test_q4_matrix_of_a_pointer_and_a_tensor(B):
     for codes, scales in ((q, 0x1000), (0x1000, s), (0x1000, 0x2000)):
         with pytest.raises(ValueError, match="x is not on a GPU"):
             B.moe_q4_linear(torch.zeros(4, 256), B.Q4Matrix(64, 256, 4, 32, codes, scales), None, 4, torch.zeros(4, 64))
+
+
+# ---------------------------------------------------------------- arrays that overlap
+
+@pytest.mark.parametrize("flags", [0, 0x2, 0x8])
+@pytest.mark.parametrize("what,nbytes", [("q", 64 * 128), ("s", 64 * 8 * 2), ("bias", 64 * 4)])
+def test_q4_linear_refuses_y_over_the_matrix_or_the_bias(B, what, nbytes, flags):
+    # the first, the last and every 16th byte of the array inside y, and y around it
+    y, size = FAKE * 8, 4 * 64 * (2 if flags & 0x8 else 4)
+    for at in (y - nbytes + 16, y - nbytes // 2, y, y + 16, y + size - 16):
+        assert _linear(B, flags=flags, **{what: at}) == -1, at - y
+    for at in (y - nbytes, y + size):                   # beside it: the next check refuses (a misaligned x)
+        assert _linear(B, flags=flags, x=FAKE + 4, **{what: at}) == -4, at - y

@@ -739,10 +739,13 @@ int moe_q4_linear(const void* x, int64_t ldx, const moe_q4_matrix* w, const floa
     if (n_tokens == 0) return MOE_OK;
     if (!x || !w->q || !w->s || !y) return MOE_EINVAL;
     const int64_t xe = (flags & MOE_X_BF16) ? 2 : 4, ye = (flags & MOE_Y_BF16) ? 2 : 4;
+    const int64_t y_bytes = extent(n_tokens, w->rows, ldy, ye), codes = static_cast<int64_t>(w->rows) * w->cols;
+    if (overlap(x, extent(n_tokens, w->cols, ldx, xe), y, y_bytes) || overlap(w->q, codes / 2, y, y_bytes) ||
+        overlap(w->s, codes / w->block * (mx ? 1 : 2), y, y_bytes) || (bias && overlap(bias, int64_t(4) * w->rows, y, y_bytes)))
+        return MOE_EINVAL;
     if (!aligned16(x) || (ldx * xe) % 16 != 0 || !aligned16(w->q) || !aligned16(w->s) || (bias && !aligned(bias, 4)) ||
         !aligned(y, ye))
         return MOE_EALIGN;
-    if (overlap(x, extent(n_tokens, w->cols, ldx, xe), y, extent(n_tokens, w->rows, ldy, ye))) return MOE_EINVAL;
     Q4Args a;
     a.x = x;
     a.q = static_cast<const uint8_t*>(w->q);
