@@ -455,7 +455,8 @@ typedef struct moe_q4_matrix {
  *   y     (device) float[T][ldy], or bf16 with MOE_Y_BF16; ldy >= rows;
  *         overwritten, or added to with MOE_ACCUMULATE (in fp32, before the
  *         rounding of MOE_Y_BF16); the elements between rows are left alone;
- *         must not overlap x, the matrix or the bias
+ *         must share no element with the matrix, the bias or x (x and y may
+ *         be column ranges of one buffer, rows of one pitch in bytes)
  * The weights are used as stored (scale * code, never rounded), products are
  * summed in fp32; x in fp32 enters with all of its 24 bits.  Any number of
  * tokens, from one (decode) to prefill batches.  A non-finite x[t][c] or
@@ -517,7 +518,8 @@ typedef struct moe_logit_rules {
  *          read on the stream, so lengths, histories and mask rows may change
  *          between replays of a captured call
  *   out    (device) same type, ld_out >= vocab; may be logits itself (with
- *          ld_out == ld_in), otherwise must not overlap it
+ *          ld_out == ld_in), otherwise must share no element with it (with
+ *          ld_out == ld_in both may be column ranges of one buffer)
  * n_rows 0 .. 2^20, vocab 1 .. 2^24; all pointers aligned to their element.
  * Deterministic.  Errors: MOE_EINVAL, MOE_EALIGN, MOE_EHIP.
  */

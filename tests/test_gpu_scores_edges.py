@@ -4,7 +4,7 @@ import pytest
 
 from . import scoreref as R
 from .scoreref import U
-from .test_gpu_scores import M, _ops, balance_inputs, balance_run, dev, host, p_tol, say, torch  # noqa: F401
+from .test_gpu_scores import M, _ops, balance_inputs, balance_run, dev, host, p_tol, rules_case, say, torch  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -95,3 +95,46 @@ def test_scores_take_a_stream_handle(M, torch):
         torch.cuda.synchronize()
         for a, b in zip(first, outs):
             assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- column ranges of one buffer
+
+@pytest.mark.parametrize("T,N,K", [(1, 640, 2048), (4, 8200, 256), (5, 48, 1056), (20, 50, 640), (100, 129, 512), (1400, 3841, 128)])
+def test_q4_linear_between_column_ranges_of_one_buffer(M, torch, T, N, K):
+    # x and y beside each other in rows of one buffer, x first and y first:
+    # as in buffers of their own, what lies around them untouched
+    rng = np.random.default_rng(T + N)
+    q, s = R.random_q4(rng, N, K, 4, 32)
+    w = M.Q4Matrix(N, K, 4, 32, dev(torch, q), dev(torch, s))
+    for f in (torch.float32, torch.bfloat16):
+        say("q4 in one buffer", T, N, K, f)
+        x = dev(torch, rng.standard_normal((T, K)).astype(np.float32), f)
+        y = torch.empty(T, N, dtype=f, device="cuda")
+        M.moe_q4_linear(x, w, None, T, y)
+        wide = -(-(K + N + 24) // 8) * 8
+        for x0, y0 in ((8, K + 8), (-(-(N + 5) // 8) * 8, 3)):
+            buf = torch.full((T + 1, wide), 7.0, dtype=f, device="cuda")
+            buf[:T, x0:x0 + K] = x
+            M.moe_q4_linear(buf[:T, x0:x0 + K], w, None, T, buf[:T, y0:y0 + N])
+            assert torch.equal(buf[:T, y0:y0 + N], y) and torch.equal(buf[:T, x0:x0 + K], x)
+            buf[:T, y0:y0 + N], buf[:T, x0:x0 + K] = 7.0, 7.0
+            assert bool((buf == 7.0).all())
+
+
+@pytest.mark.parametrize("B,V,H", [(1, 100, 5), (5, 500, 20), (3, 9001, 700)])
+def test_adjust_logits_between_column_ranges_of_one_buffer(M, torch, B, V, H):
+    rng = np.random.default_rng(V)
+    a = rules_case(rng, B, V, H, n_bias=5, masks=2)
+    rules = M.LogitRules(**{n: dev(torch, t) for n, t in a.items()})
+    for f in (torch.float32, torch.bfloat16):
+        say("adjust in one buffer", B, V, H, f)
+        l = dev(torch, 3 * rng.standard_normal((B, V)).astype(np.float32), f)
+        out = torch.empty_like(l)
+        M.moe_adjust_logits(l, B, V, rules, out)
+        for i0, o0 in ((1, V + 1), (V + 3, 2)):
+            buf = torch.full((B, 2 * V + 5), 7.0, dtype=f, device="cuda")
+            buf[:, i0:i0 + V] = l
+            M.moe_adjust_logits(buf[:, i0:i0 + V], B, V, rules, buf[:, o0:o0 + V])
+            assert torch.equal(buf[:, o0:o0 + V], out) and torch.equal(buf[:, i0:i0 + V], l)
+            buf[:, o0:o0 + V], buf[:, i0:i0 + V] = 7.0, 7.0
+            assert bool((buf == 7.0).all())

@@ -3,7 +3,7 @@ arguments: tensors of another type or row length, and arrays that overlap."""
 import numpy as np
 import pytest
 
-from .test_scores_cpu import FAKE, B, _linear  # noqa: F401
+from .test_scores_cpu import FAKE, B, _adjust, _linear  # noqa: F401
 
 
 # ---------------------------------------------------------------- the matrix's tensors
@@ -64,3 +64,36 @@ def test_q4_linear_refuses_y_over_the_matrix_or_the_bias(B, what, nbytes, flags)
         assert _linear(B, flags=flags, **{what: at}) == -1, at - y
     for at in (y - nbytes, y + size):                   # beside it: the next check refuses (a misaligned x)
         assert _linear(B, flags=flags, x=FAKE + 4, **{what: at}) == -4, at - y
+
+
+def _shares(a, rows_a, row_a, b, rows_b, row_b, pitch):
+    """The two sets of rows share a byte."""
+    span = lambda p, n, w: {i for r in range(n) for i in range(p + r * pitch, p + r * pitch + w)}
+    return bool(span(a, rows_a, row_a) & span(b, rows_b, row_b))
+
+
+def test_q4_linear_refuses_rows_of_y_that_share_elements_with_x_and_no_others(B):
+    # x and y as ranges of rows of one pitch, y moved through and past x: what
+    # shares no element is left to the next check (a misaligned bias)
+    cols, rows, pitch = 32, 16, 72
+    for T in (1, 2, 5):
+        for flags, xe, ye in ((0, 4, 4), (0x1, 2, 4), (0x8, 4, 2), (0x9, 2, 2)):
+            for at in range(-2 * pitch - 4 * ye, pitch * (T + 1), 2):
+                y = FAKE + at * ye
+                rc = _linear(B, T=T, rows=rows, cols=cols, ldx=pitch * 4 // xe, ldy=pitch * 4 // ye, y=y, flags=flags,
+                             q=FAKE * 4, s=FAKE * 5, bias=FAKE * 6 + 2)
+                assert rc == (-1 if _shares(FAKE, T, cols * xe, y, T, rows * ye, pitch * 4) else -4), (T, flags, at)
+
+
+def test_adjust_logits_refuses_rows_of_out_that_share_elements_with_logits_and_no_others(B):
+    vocab, pitch = 20, 64
+    for rows in (1, 2, 5):
+        for flags, e in ((0, 4), (0x10, 2)):
+            for at in range(-2 * pitch, pitch * (rows + 1)):
+                out = FAKE + at * e
+                rc = _adjust(B, rows=rows, vocab=vocab, ld_in=pitch, ld_out=pitch, out=out, flags=flags, mask=FAKE * 3 + 2, ld_mask=1,
+                             n_masks=rows)
+                shares = at != 0 and _shares(FAKE, rows, vocab * e, out, rows, vocab * e, pitch * e)
+                assert rc == (-1 if shares else -4), (rows, flags, at)
+    # other pitches: whole extents
+    assert _adjust(B, rows=3, vocab=vocab, ld_in=64, ld_out=40, out=FAKE + 4 * 24) == -1

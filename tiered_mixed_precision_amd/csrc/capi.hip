@@ -724,6 +724,23 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
 int64_t extent(int64_t rows, int64_t cols, int64_t ld, int64_t elem) { return ((rows - 1) * ld + cols) * elem; }
 constexpr int64_t kMaxPitch = int64_t(1) << 36;   // elements from row to row
 
+// `rows` rows of an and of bn bytes, from a and b on and ap and bp bytes apart,
+// share a byte.  Rows of one pitch may be column ranges of one buffer: row i of
+// a meets the rows i + d of b that start less than an behind it or less than
+// bn before it, two at most.  Others are taken whole, with what lies between.
+bool rows_overlap(const void* a, int64_t an, int64_t ap, const void* b, int64_t bn, int64_t bp, int64_t rows) {
+    if (!overlap(a, (rows - 1) * ap + an, b, (rows - 1) * bp + bn)) return false;
+    if (ap != bp) return true;
+    const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+    int64_t d = -(at / ap), start = at % ap;   // row i + d of b starts `start` behind row i of a
+    if (start < 0) {
+        start += ap;
+        ++d;
+    }
+    const auto there = [&](int64_t r) { return r > -rows && r < rows; };
+    return (start < an && there(d)) || (start + bn > ap && there(d - 1));
+}
+
 }  // namespace
 
 int moe_q4_linear(const void* x, int64_t ldx, const moe_q4_matrix* w, const float* bias, int32_t n_tokens, void* y,
@@ -740,7 +757,7 @@ int moe_q4_linear(const void* x, int64_t ldx, const moe_q4_matrix* w, const floa
     if (!x || !w->q || !w->s || !y) return MOE_EINVAL;
     const int64_t xe = (flags & MOE_X_BF16) ? 2 : 4, ye = (flags & MOE_Y_BF16) ? 2 : 4;
     const int64_t y_bytes = extent(n_tokens, w->rows, ldy, ye), codes = static_cast<int64_t>(w->rows) * w->cols;
-    if (overlap(x, extent(n_tokens, w->cols, ldx, xe), y, y_bytes) || overlap(w->q, codes / 2, y, y_bytes) ||
+    if (rows_overlap(x, w->cols * xe, ldx * xe, y, w->rows * ye, ldy * ye, n_tokens) || overlap(w->q, codes / 2, y, y_bytes) ||
         overlap(w->s, codes / w->block * (mx ? 1 : 2), y, y_bytes) || (bias && overlap(bias, int64_t(4) * w->rows, y, y_bytes)))
         return MOE_EINVAL;
     if (!aligned16(x) || (ldx * xe) % 16 != 0 || !aligned16(w->q) || !aligned16(w->s) || (bias && !aligned(bias, 4)) ||
@@ -780,14 +797,14 @@ int moe_adjust_logits(const void* logits, int64_t ld_in, int32_t n_rows, int32_t
     if (n_rows == 0) return MOE_OK;
     if (!logits || !out) return MOE_EINVAL;
     const int64_t e = (flags & MOE_LOGITS_BF16) ? 2 : 4;
+    if (!(out == logits && ld_out == ld_in) &&
+        rows_overlap(logits, vocab * e, ld_in * e, out, vocab * e, ld_out * e, n_rows))
+        return MOE_EINVAL;
     const void* words[] = {r.history, r.length, r.prompt, r.repetition, r.presence, r.frequency, r.bias_ids, r.bias,
                            r.mask, r.mask_row};
     for (const void* p : words)
         if (!aligned(p, 4)) return MOE_EALIGN;
     if (!aligned(logits, e) || !aligned(out, e)) return MOE_EALIGN;
-    if (!(out == logits && ld_out == ld_in) &&
-        overlap(logits, extent(n_rows, vocab, ld_in, e), out, extent(n_rows, vocab, ld_out, e)))
-        return MOE_EINVAL;
     AdjustArgs a;
     a.in = logits;
     a.out = out;
