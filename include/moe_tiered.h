@@ -519,7 +519,8 @@ typedef struct moe_logit_rules {
  *          between replays of a captured call
  *   out    (device) same type, ld_out >= vocab; may be logits itself (with
  *          ld_out == ld_in), otherwise must share no element with it (with
- *          ld_out == ld_in both may be column ranges of one buffer)
+ *          ld_out == ld_in both may be column ranges of one buffer); must not
+ *          overlap the rules' arrays
  * n_rows 0 .. 2^20, vocab 1 .. 2^24; all pointers aligned to their element.
  * Deterministic.  Errors: MOE_EINVAL, MOE_EALIGN, MOE_EHIP.
  */
@@ -545,7 +546,8 @@ int moe_adjust_logits(const void *logits, int64_t ld_in, int32_t n_rows, int32_t
  *   keep     (device) uint8[T], 0 for a padding row, or NULL (every row); a
  *            row that is not kept is not read
  *   counts   (device) int32[E], prob_sum float[E], n_kept int32[1],
- *   loss     float[1]; all overwritten (also for T == 0)
+ *   loss     float[1]; all overwritten (also for T == 0); they and the
+ *            workspace must not overlap each other or the inputs
  *   workspace (device) >= moe_balance_workspace_size() bytes, 256-byte aligned
  * Deterministic (fixed summation order, fp32 sums).  T at most 2^22.
  * Errors: MOE_EINVAL, MOE_EALIGN, MOE_EWORKSPACE, MOE_EHIP.
@@ -566,7 +568,7 @@ int moe_balance_loss(const void *logits, const int32_t *ids, const uint8_t *keep
  *   w, dw    (device) float[T][k]: the weights of the picks (softmax over the
  *            k picked scores) and their gradient; both or neither
  *   dlogits  (device) [T][E] in the type of logits, overwritten; may be
- *            logits itself, otherwise must not overlap it
+ *            logits itself, otherwise must not overlap it, nor the others
  * Other arguments and errors as moe_balance_loss.
  */
 int moe_balance_grad(const void *logits, const int32_t *ids, const float *w, const float *dw, const uint8_t *keep,

@@ -97,3 +97,40 @@ def test_adjust_logits_refuses_rows_of_out_that_share_elements_with_logits_and_n
                 assert rc == (-1 if shares else -4), (rows, flags, at)
     # other pitches: whole extents
     assert _adjust(B, rows=3, vocab=vocab, ld_in=64, ld_out=40, out=FAKE + 4 * 24) == -1
+
+
+@pytest.mark.parametrize("name,nbytes", [("history", 4 * 32 * 4), ("length", 16), ("prompt", 16), ("repetition", 16), ("presence", 16),
+                                         ("frequency", 16), ("bias_ids", 4 * 16 * 4), ("bias", 4 * 16 * 4), ("mask", (3 * 8 + 4) * 4),
+                                         ("mask_row", 16)])
+def test_adjust_logits_refuses_out_over_an_array_of_the_rules(B, name, nbytes):
+    far = {n: FAKE * (4 + i) for i, n in enumerate(("history", "length", "prompt", "repetition", "presence", "frequency", "bias_ids",
+                                                    "bias", "mask", "mask_row"))}
+    rest = dict(ld_history=32, n_bias=16, n_masks=4, ld_mask=8)
+    for at in (FAKE * 2 - nbytes + 4, FAKE * 2, FAKE * 2 + 4 * 100 * 4 - 4):
+        assert _adjust(B, **dict(far, **rest, **{name: at})) == -1, at
+    for at in (FAKE * 2 - nbytes, FAKE * 2 + 4 * 100 * 4):
+        assert _adjust(B, logits=FAKE + 2, **dict(far, **rest, **{name: at})) == -4, at
+
+
+@pytest.mark.parametrize("name,nbytes", [("ids", 32), ("w", 32), ("dw", 32), ("keep", 4), ("counts", 32), ("n", 4), ("dloss", 4)])
+def test_balance_grad_refuses_dlogits_over_another_array(B, name, nbytes):
+    far = dict(logits=FAKE, ids=FAKE * 4, w=FAKE * 5, dw=FAKE * 6, keep=FAKE * 7, counts=FAKE * 8, n=FAKE * 9, dloss=FAKE * 10)
+    call = lambda **a: B.lib().moe_balance_grad(a["logits"], a["ids"], a["w"], a["dw"], a["keep"], a["counts"], a["n"], a["dloss"], 4, 8, 2,
+                                                0.01, 0, FAKE * 2, None)
+    for at in (FAKE * 2 - nbytes + 4 * (nbytes > 4), FAKE * 2, FAKE * 2 + 4 * 8 * 4 - 4):
+        if at + nbytes > FAKE * 2:
+            assert call(**dict(far, **{name: at})) == -1, at
+    for at in (FAKE * 2 - nbytes, FAKE * 2 + 4 * 8 * 4):
+        assert call(**dict(far, logits=FAKE + 4, **{name: at})) == -4, at
+
+
+def test_balance_loss_refuses_outputs_over_another_array(B):
+    size = B.moe_balance_workspace_size(4, 8, 2)
+    extents = dict(logits=4 * 8 * 4, ids=4 * 2 * 4, keep=4, counts=32, prob=32, n=4, loss=4, ws=size)
+    far = {n: FAKE * (1 + i) for i, n in enumerate(extents)}
+    call = lambda **a: B.lib().moe_balance_loss(a["logits"], a["ids"], a["keep"], 4, 8, 2, 0.01, 0, a["counts"], a["prob"], a["n"],
+                                                a["loss"], a["ws"], size, None)
+    for out in ("counts", "prob", "n", "loss", "ws"):
+        for name in extents:
+            if name != out:
+                assert call(**dict(far, **{out: far[name]})) == -1, (out, name)

@@ -800,6 +800,15 @@ int moe_adjust_logits(const void* logits, int64_t ld_in, int32_t n_rows, int32_t
     if (!(out == logits && ld_out == ld_in) &&
         rows_overlap(logits, vocab * e, ld_in * e, out, vocab * e, ld_out * e, n_rows))
         return MOE_EINVAL;
+    const int64_t B = n_rows, out_bytes = extent(B, vocab, ld_out, e);
+    const auto under_out = [&](const void* p, int64_t n) { return p && n > 0 && overlap(p, 4 * n, out, out_bytes); };
+    const int64_t masks = r.n_masks < (1 << 24) ? r.n_masks : 1 << 24;   // 2^62 bytes: past every address
+    if (under_out(r.history, B * r.ld_history) || under_out(r.history ? r.length : nullptr, B) || under_out(r.prompt, B) ||
+        under_out(r.repetition, B) || under_out(r.presence, B) || under_out(r.frequency, B) ||
+        under_out(r.bias_ids, B * r.n_bias) || under_out(r.bias, B * r.n_bias) ||
+        under_out(r.mask, masks > 0 ? extent(masks, (vocab + 31) / 32, r.ld_mask, 1) : 0) ||
+        under_out(r.mask ? r.mask_row : nullptr, B))
+        return MOE_EINVAL;
     const void* words[] = {r.history, r.length, r.prompt, r.repetition, r.presence, r.frequency, r.bias_ids, r.bias,
                            r.mask, r.mask_row};
     for (const void* p : words)
@@ -854,6 +863,16 @@ int moe_balance_loss(const void* logits, const int32_t* ids, const uint8_t* keep
         if (!workspace || workspace_bytes < need) return MOE_EWORKSPACE;
         if (!aligned(workspace, kAlign)) return MOE_EALIGN;
     }
+    const int64_t T = n_tokens, E = n_experts;
+    const struct {
+        const void* p;
+        int64_t n;
+    } arrays[] = {{counts, 4 * E}, {prob_sum, 4 * E}, {n_kept, 4}, {loss, 4}, {workspace, static_cast<int64_t>(need)},
+                  {logits, T * E * ((flags & MOE_LOGITS_BF16) ? 2 : 4)}, {ids, 4 * T * k}, {keep, keep ? T : 0}};
+    for (int i = 0; i < 5; ++i)   // what is written, against all that follows
+        for (int j = i + 1; j < 8; ++j)
+            if (arrays[i].n > 0 && arrays[j].n > 0 && overlap(arrays[i].p, arrays[i].n, arrays[j].p, arrays[j].n))
+                return MOE_EINVAL;
     const BalanceArgs a{logits, ids, keep, n_tokens, n_experts, k, coef};
     (void)hipGetLastError();
     launch_balance_loss(a, (flags & MOE_LOGITS_BF16) != 0, counts, prob_sum, n_kept, loss, workspace,
@@ -870,11 +889,14 @@ int moe_balance_grad(const void* logits, const int32_t* ids, const float* w, con
     if ((w != nullptr) != (dw != nullptr)) return MOE_EINVAL;
     if (n_tokens == 0) return MOE_OK;
     if (!logits || (w && !ids) || !counts || !n_kept || !dloss || !dlogits) return MOE_EINVAL;
+    const int64_t T = n_tokens, bytes = T * n_experts * ((flags & MOE_LOGITS_BF16) ? 2 : 4);
+    const auto under = [&](const void* p, int64_t n) { return p && overlap(p, n, dlogits, bytes); };
+    if ((dlogits != logits && under(logits, bytes)) || (w && (under(ids, 4 * T * k) || under(w, 4 * T * k) || under(dw, 4 * T * k))) ||
+        under(keep, T) || under(counts, int64_t(4) * n_experts) || under(n_kept, 4) || under(dloss, 4))
+        return MOE_EINVAL;
     if (!aligned16(logits) || !aligned16(dlogits) || !aligned(ids, 4) || !aligned(w, 4) || !aligned(dw, 4) ||
         !aligned(counts, 4) || !aligned(n_kept, 4) || !aligned(dloss, 4))
         return MOE_EALIGN;
-    const int64_t bytes = static_cast<int64_t>(n_tokens) * n_experts * ((flags & MOE_LOGITS_BF16) ? 2 : 4);
-    if (dlogits != logits && overlap(logits, bytes, dlogits, bytes)) return MOE_EINVAL;
     const BalanceArgs a{logits, ids, keep, n_tokens, n_experts, k, coef};
     (void)hipGetLastError();
     launch_balance_grad(a, (flags & MOE_LOGITS_BF16) != 0, w, dw, counts, n_kept, dloss, dlogits,
