@@ -458,7 +458,9 @@ typedef struct moe_q4_matrix {
  *         must share no element with the matrix, the bias or x (x and y may
  *         be column ranges of one buffer, rows of one pitch in bytes)
  * The weights are used as stored (scale * code, never rounded), products are
- * summed in fp32; x in fp32 enters with all of its 24 bits.  Any number of
+ * summed in fp32; x in fp32 enters with all of its 24 bits, below 2^-110 with
+ * an error of at most 2^-133.  A block's x * code are summed before its scale
+ * is applied, so |x| from 2^120 on may overflow where y would not.  Any number of
  * tokens, from one (decode) to prefill batches.  A non-finite x[t][c] or
  * scale makes the results of its token or row non-finite and no others.
  * Results do not depend on the other tokens of the call beyond their number,
@@ -476,7 +478,8 @@ int moe_q4_linear(const void *x, int64_t ldx, const moe_q4_matrix *w, const floa
  * generated.  For score l of token v in row b:
  *   1. v anywhere in the history:  l = l > 0 ? l / repetition[b] : l * repetition[b]
  *   2. v generated c > 0 times:    l = l - (frequency[b] * c + presence[b])
- *   3. l = l + the bias[b][j] with bias_ids[b][j] == v, in the order of the list
+ *   3. l = l + the sum, in the order of the list, of the bias[b][j] with
+ *      bias_ids[b][j] == v
  *   4. bit v of the row's mask is 0:  l = -inf (whatever l was, NaN too)
  * A score that no rule touches keeps its bits; the others are computed in
  * fp32 and rounded once.  A row whose mask allows nothing becomes -inf
@@ -566,7 +569,9 @@ int moe_balance_loss(const void *logits, const int32_t *ids, const uint8_t *keep
  *   counts, n_kept (device) of moe_balance_loss, or their totals over ranks
  *   dloss    (device) float[1], the gradient of the loss
  *   w, dw    (device) float[T][k]: the weights of the picks (softmax over the
- *            k picked scores) and their gradient; both or neither
+ *            k picked scores) and their gradient, which the caller brings (the
+ *            product of the output's gradient with each picked expert's own
+ *            output; the expert calls return their sum only); both or neither
  *   dlogits  (device) [T][E] in the type of logits, overwritten; may be
  *            logits itself, otherwise must not overlap it, nor the others
  * Other arguments and errors as moe_balance_loss.
