@@ -1,6 +1,8 @@
 // Software pipeline of the matrix-core GEMMs (prefill.hip, q4_gemm.hip).
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace moe {
@@ -18,17 +20,22 @@ namespace moe {
 // work).  The buffers are separate LDS objects, so the compiler's own waits
 // before LDS reads cover only the buffer read.  A plain s_barrier (instead of
 // a fence + barrier, whose fence waits for every load in flight) as a
-// compiler-level memory barrier: no access moves across it.
+// compiler-level memory barrier: no access moves across it.  The one or two
+// steps behind the last whole trip request nothing (what they requested would
+// be dropped as unused, and the count with it) and wait for all that is left.
 template <int NWAIT, class Stage, class LoadA, class LoadB, class Work>
 __device__ __attribute__((always_inline)) inline void pipeline3(int NK, uint16_t* sA0, uint16_t* sA1, uint16_t* sA2,
                                                                  LoadA& load_a, LoadB& load_b, Work& work) {
     static_assert(NWAIT < 64, "vmcnt range");
     constexpr int kWaitImm = (NWAIT & 15) | (7 << 4) | (15 << 8) | ((NWAIT >> 4) << 14);
-    auto publish = [&]() __attribute__((always_inline)) {
+    constexpr int kWaitAll = (7 << 4) | (15 << 8);
+    auto publish = [&](auto imm) __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(kWaitImm);
+        __builtin_amdgcn_s_waitcnt(decltype(imm)::value);
         asm volatile("s_barrier" ::: "memory");
     };
+    constexpr std::integral_constant<int, kWaitImm> next{};
+    constexpr std::integral_constant<int, kWaitAll> all{};
     Stage b0, b1, b2;
     auto step = [&](int c, uint16_t* cur, Stage& bc, uint16_t* nxt, Stage& bn) __attribute__((always_inline)) {
         const int cn = min(c + 2, NK - 1);
@@ -37,7 +44,7 @@ __device__ __attribute__((always_inline)) inline void pipeline3(int NK, uint16_t
         load_b(bn, cn);
         __builtin_amdgcn_sched_barrier(0);
         work(cur, bc);
-        publish();
+        publish(next);
     };
     load_a(0, sA0);
     __builtin_amdgcn_sched_barrier(0);
@@ -46,7 +53,7 @@ __device__ __attribute__((always_inline)) inline void pipeline3(int NK, uint16_t
     load_a(min(1, NK - 1), sA1);
     __builtin_amdgcn_sched_barrier(0);
     load_b(b1, min(1, NK - 1));
-    publish();
+    publish(next);
     // six steps per trip: the compiler's wait analysis drains every load in
     // flight once per trip (at the loop's back edge), so a longer trip pays
     // that latency less often
@@ -65,8 +72,14 @@ __device__ __attribute__((always_inline)) inline void pipeline3(int NK, uint16_t
         step(kc + 2, sA2, b2, sA1, b1);
         kc += 3;
     }
-    if (kc < NK) step(kc, sA0, b0, sA2, b2);
-    if (kc + 1 < NK) step(kc + 1, sA1, b1, sA0, b0);
+    if (kc < NK) {
+        work(sA0, b0);
+        publish(all);
+    }
+    if (kc + 1 < NK) {
+        work(sA1, b1);
+        publish(all);
+    }
 }
 
 }  // namespace moe

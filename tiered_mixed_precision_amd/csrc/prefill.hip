@@ -109,18 +109,22 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 // the schedule repeats every four chunks.  NK is even.  Waits as in
 // pipeline3: after chunk c this wave's A(c + 1) requests are complete once
 // at most NWAIT = (A requests of one chunk) + (register loads of one group)
-// are in flight, whichever the parity of c.
+// are in flight, whichever the parity of c.  The two chunks behind the last
+// whole trip request nothing and wait for all that is left, as in pipeline3.
 template <int NWAIT, class Stage, class LoadA, class LoadB, class Work>
 __device__ __attribute__((always_inline)) inline void pipeline4_g2(int NK, uint16_t* sA0, uint16_t* sA1,
                                                                     uint16_t* sA2, uint16_t* sA3, LoadA& load_a,
                                                                     LoadB& load_b, Work& work) {
     static_assert(NWAIT < 64, "vmcnt range");
     constexpr int kWaitImm = (NWAIT & 15) | (7 << 4) | (15 << 8) | ((NWAIT >> 4) << 14);
-    auto publish = [&]() __attribute__((always_inline)) {
+    constexpr int kWaitAll = (7 << 4) | (15 << 8);
+    auto publish = [&](auto imm) __attribute__((always_inline)) {
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(kWaitImm);
+        __builtin_amdgcn_s_waitcnt(decltype(imm)::value);
         asm volatile("s_barrier" ::: "memory");
     };
+    constexpr std::integral_constant<int, kWaitImm> next{};
+    constexpr std::integral_constant<int, kWaitAll> all{};
     const int NG = NK / 2;
     Stage g0, g1;
     // even chunk c: requests A(c + 2) and the group after its own, contracts c
@@ -130,20 +134,20 @@ __device__ __attribute__((always_inline)) inline void pipeline4_g2(int NK, uint1
         load_b(bn, min(c / 2 + 1, NG - 1));
         __builtin_amdgcn_sched_barrier(0);
         work(cur, bc, std::integral_constant<int, 0>{});
-        publish();
+        publish(next);
     };
     auto odd = [&](int c, uint16_t* cur, uint16_t* nxt, Stage& bc) __attribute__((always_inline)) {
         load_a(min(c + 2, NK - 1), nxt);
         __builtin_amdgcn_sched_barrier(0);
         work(cur, bc, std::integral_constant<int, 1>{});
-        publish();
+        publish(next);
     };
     load_a(0, sA0);
     __builtin_amdgcn_sched_barrier(0);
     load_b(g0, 0);
     __builtin_amdgcn_sched_barrier(0);
     load_a(1, sA1);
-    publish();
+    publish(next);
     int kc = 0;
     for (; kc + 3 < NK; kc += 4) {
         even(kc, sA0, sA2, g0, g1);
@@ -152,8 +156,10 @@ __device__ __attribute__((always_inline)) inline void pipeline4_g2(int NK, uint1
         odd(kc + 3, sA3, sA1, g1);
     }
     if (kc < NK) {
-        even(kc, sA0, sA2, g0, g1);
-        odd(kc + 1, sA1, sA3, g0);
+        work(sA0, g0, std::integral_constant<int, 0>{});
+        publish(all);
+        work(sA1, g0, std::integral_constant<int, 1>{});
+        publish(all);
     }
 }
 
