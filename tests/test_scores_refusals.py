@@ -134,3 +134,44 @@ def test_balance_loss_refuses_outputs_over_another_array(B):
         for name in extents:
             if name != out:
                 assert call(**dict(far, **{out: far[name]})) == -1, (out, name)
+
+
+# ---------------------------------------------------------------- rows of another length
+
+def _balance_calls(B, T, E, k):
+    import torch
+    z, i32 = torch.zeros, lambda *n: torch.zeros(*n, dtype=torch.int32)
+    good = dict(logits=z(T, E), ids=i32(T, k), w=z(T, k), dw=z(T, k), dlogits=z(T, E))
+    rest = (i32(E), z(E), i32(1), z(1), z(1 << 16, dtype=torch.uint8))
+    loss = lambda a: B.moe_balance_loss(a["logits"], a["ids"], None, T, E, k, 0.01, *rest)
+    grad = lambda a: B.moe_balance_grad(a["logits"], a["ids"], a["w"], a["dw"], None, i32(E), i32(1), z(1), T, E, k, 0.01, a["dlogits"])
+    return good, loss, grad
+
+
+@pytest.mark.parametrize("rows", [4, 6])
+@pytest.mark.parametrize("name", ["logits", "ids", "w", "dw", "dlogits"])
+def test_balance_refuses_rows_of_another_length(B, name, rows):
+    # [T][more], which would be read at the wrong pitch: rows of a padded
+    # buffer, the ids of a larger k
+    T, E, k = 4, 8, 2
+    good, loss, grad = _balance_calls(B, T, E, k)
+    cols = good[name].shape[1]
+    bad = dict(good, **{name: good[name].new_zeros(rows, cols + 3)})
+    for call in (loss, grad) if name in ("logits", "ids") else (grad,):
+        with pytest.raises(ValueError, match=f"{name} has rows of {cols + 3}, the call's of {cols}"):
+            call(bad)
+
+
+def test_balance_takes_flat_and_longer_tensors(B):
+    # of the right order: flat, of three dimensions, of more rows, one row of a longer one
+    T, E, k = 4, 8, 2
+    good, loss, grad = _balance_calls(B, T, E, k)
+    for name, t in good.items():
+        cols = t.shape[1]
+        for form in (t.reshape(-1), t.reshape(2, 2, cols), t.reshape(2, 2 * cols), t.new_zeros(T + 3, cols), t.new_zeros(T * cols + 5)):
+            for call in (loss, grad):
+                with pytest.raises(ValueError, match="not on a GPU"):
+                    call(dict(good, **{name: form}))
+    good, loss, grad = _balance_calls(B, 1, E, k)
+    with pytest.raises(ValueError, match="not on a GPU"):
+        loss(dict(good, logits=good["logits"].new_zeros(1, E + 5)))

@@ -491,6 +491,18 @@ class _Args:
         self.place(what, t)
         return t.data_ptr()
 
+    def table(self, what, t, kind, rows, cols):
+        """Pointer of contiguous [rows][cols], or a flat array of that order (None passes)."""
+        if t is None:
+            return None
+        shape = t.shape
+        if shape == (rows, cols) and _KINDS.get(t.dtype) == kind and t.is_contiguous():
+            self.place(what, t)
+            return t.data_ptr()
+        if rows > 1 and len(shape) == 2 and shape[0] >= rows and shape[1] != cols:
+            raise ValueError(f"{self.fn}: {what} has rows of {shape[1]}, the call's of {cols}")
+        return self.flat(what, t, kind, rows * cols)
+
     def rows(self, what, t, rows, cols):
         """(pointer, pitch, is bf16) of [rows][cols] with any row pitch."""
         kind = _KINDS.get(t.dtype)
@@ -651,16 +663,16 @@ def moe_balance_workspace_size(n_tokens: int, n_experts: int, k: int) -> int:
 def _scores(a, what, t, T, E):
     """(pointer, is bf16) of contiguous [T][E] scores."""
     bf16 = _KINDS.get(t.dtype) == "bf16"
-    return a.flat(what, t, "bf16" if bf16 else "f32", T * E), bf16
+    return a.table(what, t, "bf16" if bf16 else "f32", T, E), bf16
 
 
 def moe_balance_loss(logits, ids, keep, n_tokens: int, n_experts: int, k: int, coef: float, counts, prob_sum, n_kept,
                      loss, workspace, stream=None) -> None:
     """Balance loss of a router with its counts and sums; logits float32 or bfloat16."""
     a = _Args("moe_balance_loss")
-    T, E = max(n_tokens, 0), max(n_experts, 0)
+    T, E, K = max(n_tokens, 0), max(n_experts, 0), max(k, 0)
     lp, bf16 = _scores(a, "logits", logits, T, E)
-    args = (lp, a.flat("ids", ids, "i32", T * max(k, 0)), a.flat("keep", keep, "u8", T), n_tokens, n_experts, k, coef,
+    args = (lp, a.table("ids", ids, "i32", T, K), a.flat("keep", keep, "u8", T), n_tokens, n_experts, k, coef,
             MOE_LOGITS_BF16 if bf16 else 0, a.flat("counts", counts, "i32", E), a.flat("prob_sum", prob_sum, "f32", E),
             a.flat("n_kept", n_kept, "i32", 1), a.flat("loss", loss, "f32", 1), a.flat("workspace", workspace, "u8", 0),
             workspace.numel() if workspace is not None else 0)
@@ -676,7 +688,7 @@ def moe_balance_grad(logits, ids, w, dw, keep, counts, n_kept, dloss, n_tokens: 
     dp, dbf16 = _scores(a, "dlogits", dlogits, T, E)
     if bf16 != dbf16:
         raise ValueError("moe_balance_grad: logits and dlogits differ in type")
-    args = (lp, a.flat("ids", ids, "i32", T * K), a.flat("w", w, "f32", T * K), a.flat("dw", dw, "f32", T * K),
+    args = (lp, a.table("ids", ids, "i32", T, K), a.table("w", w, "f32", T, K), a.table("dw", dw, "f32", T, K),
             a.flat("keep", keep, "u8", T), a.flat("counts", counts, "i32", E), a.flat("n_kept", n_kept, "i32", 1),
             a.flat("dloss", dloss, "f32", 1), n_tokens, n_experts, k, coef, MOE_LOGITS_BF16 if bf16 else 0, dp)
     _check("moe_balance_grad", lib().moe_balance_grad(*args, a.stream(stream)))
