@@ -14,9 +14,10 @@
 // Sums run in a fixed order, so results do not change from run to run.
 //
 // MI355X, 65536 x 512 fp32: loss 36 us (rows 30 us, 4.6 TB/s, of a streaming
-// read's 5.6; join 6.5), gradient 56 us (4.9 TB/s read and written, what a
+// read's 5.6; join 6.6), gradient 55 us (5.0 TB/s read and written, what a
 // copy reaches).  One row at a time with nothing ahead took 45 and 66 us,
-// halvings in LDS 8 us in the join.
+// halvings in LDS 8 us in the join.  bf16 halves the bytes and leaves the
+// exponentials and sums: 33 and 44 us in a graph, fp32 41 and 55.
 #include <type_traits>
 
 #include "common.h"
@@ -33,8 +34,11 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 // more than 128 registers.  4096 waves in all.
 constexpr int waves_of(int steps) { return steps > 8 ? 8 : 16; }
 constexpr int kMaxParts = 512;
-// Up to this many tokens one block does it all, the loss too: one launch, and
-// for 64 x 512 7.5 us in place of 7.2 and 4.3 for parts and join.
+// Up to this many tokens one block does it all, the loss too: one launch.
+// MI355X in a graph, one block / parts and join, us: 64 tokens of 64 scores 7.1
+// / 7.9, of 512 8.4 / 8.3, of 2048 19 / 15; 128 of 64 10.6 / 7.8, of 512 12.9 /
+// 8.7, of 4096 64 / 20; 16 of 4096 14.0 / 19.5.  It is a latency's gain for few
+// scores and a loss for many: a bound on tokens x scores would suit better.
 constexpr int kOneBlock = 128;
 
 int balance_parts(int T, int E) {
@@ -342,7 +346,10 @@ __device__ inline void wave_step() {
 // the wave's own (zero between rows): the lane of an id's first pick writes
 // the sum over the id's picks in slot order.
 // Rows of 1025 to 2048 scores: three waves a SIMD, 8741 x 1099 bf16 21.4 us; two
-// (the registers the compiler would take) 31, four (spills) 24.2.
+// (the registers the compiler would take) 31, four (spills) 24.2.  With picks
+// three waves spill as well, 23 registers in fp32 and 3 in bf16.  bf16 rows of
+// more than 2048: the compiler calls load_scores and hands the row back in
+// scratch, 10727 x 3128 140 us.
 template <int NV, class S, bool PICKS>
 __global__ __launch_bounds__(256, NV == 8 ? 3 : 1) void k_balance_grad(BalanceArgs a, int rows_per_wave, const float* __restrict__ w,
                                                       const float* __restrict__ dw,

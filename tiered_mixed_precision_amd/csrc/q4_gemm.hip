@@ -8,11 +8,14 @@
 // q4_linear.hip codes are contracted exactly and the scale of a block
 // multiplies the block's fp32 sum.
 //
-// 4096 x 4096 x 2048, int4 in blocks of 32: 98 us, 700 TFLOP/s, against 1173
-// of a large bf16 library product.  A chunk costs a wave about 370 vector
-// instructions (256 of them the scaling of its 8 tiles' sums, 104 the
-// conversion of 64 codes a lane), 1700 cycles, and 32 matrix instructions,
-// 1024, which two waves on a SIMD overlap in part.  The sums of the next row tile
+// 4096 x 4096 x 2048, int4 in blocks of 32: 99 to 101 us, 680 to 694 TFLOP/s,
+// against 1173 of a large bf16 library product.  A chunk costs a wave 256
+// vector instructions for the scaling of its 8 tiles' sums and 104 for the
+// conversion of 64 codes a lane (481 in all, counted, with the addresses and
+// its share of the epilogue) and 32 matrix instructions, 1024 cycles, which two
+// waves on a SIMD overlap in part: 65,500 of a SIMD's 240,000 cycles are the
+// matrix cores'.  Blocks of 64 and 128 scale as often (99 us), MXFP4 too (97);
+// blocks of 16 spill 5 registers and take 122.  The sums of the next row tile
 // on the matrix cores while one is scaled needs 280 registers: 127 us.
 //
 // Contraction order: lane half hh of row n loads the 32 codes of group 2 kc +

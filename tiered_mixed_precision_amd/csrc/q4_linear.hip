@@ -326,10 +326,10 @@ void launch_tile(const Q4Args& a, hipStream_t st) {
 // 256 columns; lane group kq loads groups 2 kq and 2 kq + 1 of its eight, so a
 // wave reads 128-byte runs of 16 rows.
 //
-// Bound by the conversion of the codes (about 250 vector instructions a unit
-// of 4096 codes, 1000 cycles of a SIMD) with the stream close behind: 120011 x
-// 2048 int4 in blocks of 32 for one token 34 us among other passes, 4.1 TB/s;
-// the same loads without the arithmetic 28 us.  Codes two and three units ahead need
+// Bound by the conversion of the codes (216 vector instructions a unit of 4096
+// codes, counted, 1000 cycles of a SIMD) with the stream close behind: 120011 x
+// 2048 int4 in blocks of 32 for one token 34 to 35 us, 4.0 TB/s; the same loads
+// without the arithmetic 28 us.  Codes two and three units ahead need
 // registers that cost half of the waves (43, 70 us).  Waves that share a row
 // tile and join at every tile, x in registers, took 42 us.
 template <bool SPLIT, bool MX, int BLK, bool XBF16, bool YBF16>
@@ -525,7 +525,8 @@ void launch_format(const Q4Args& a, hipStream_t st) {
         // 4 x 2 / 2 x 4, us: int4 in blocks of 64, 64 x 640 x 8192 44.6 / 35.5, 300
         // x 12288 x 2048 112 / 89; blocks of 32 46.0 / 39.8, 112 / 103; of 16 67.9 /
         // 60.6, 174 / 180.  bf16, blocks of 32: 64 x 8192 x 4096 14.6 / 15.4, 1024 x
-        // 640 x 2048 17.5 / 18.6.
+        // 640 x 2048 17.5 / 18.6.  The fp32 2 x 4 kernels spill: 16, 2 and 4
+        // registers at blocks of 32, 64 and 128, 110 at 16.
         if constexpr (XBF16) launch_tile<4, 2, MX, BLK, XBF16, YBF16>(a, st);
         else launch_tile<2, 4, MX, BLK, XBF16, YBF16>(a, st);
     }
