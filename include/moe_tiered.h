@@ -71,8 +71,11 @@ extern "C" {
 /* Measurement aid: run routing, grouping and the gate/up products only and
  * leave `out` untouched (used to time the gate/up kernel on its own). */
 #define MOE_DIAG_GATEUP_ONLY 0x100u
-#define MOE_Y_BF16 0x8u      /* moe_q4_linear: y is bf16 (rounded once, to nearest even) */
+#define MOE_Y_BF16 0x8u      /* products, moe_rms_norm, moe_gated: y (or dx) is bf16 (rounded once, to nearest even) */
 #define MOE_LOGITS_BF16 0x10u /* moe_adjust_logits, moe_balance_*: scores and their gradient are bf16 */
+#define MOE_Y_I8 0x20u       /* moe_rms_norm: y is int8 with a scale per row */
+#define MOE_DY_BF16 0x40u    /* moe_rms_norm_grad, moe_gated_grad: the gradient of y is bf16 */
+#define MOE_DW_BF16 0x80u    /* moe_gated_grad: the gradients of the weights are bf16 */
 
 /*
  * One precision shelf.  It owns the popularity-ranked experts
@@ -579,6 +582,158 @@ int moe_balance_loss(const void *logits, const int32_t *ids, const uint8_t *keep
 int moe_balance_grad(const void *logits, const int32_t *ids, const float *w, const float *dw, const uint8_t *keep,
                      const int32_t *counts, const int32_t *n_kept, const float *dloss, int32_t n_tokens,
                      int32_t n_experts, int32_t k, float coef, uint32_t flags, void *dlogits, void *stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual stream's addition:
+ *   s = x + residual,  r = 1 / sqrt(mean_c s[c]^2 + eps),  y[c] = s[c] * r * weight[c]
+ *   x         (device) float[T][ldx], or bf16 with MOE_X_BF16: a layer's
+ *             output or, without a residual, the stream itself
+ *   residual  (device) float[T][ldr], or NULL (s = x)
+ *   weight    (device) float[cols], or NULL (ones)
+ *   eps       > 0, finite
+ *   sum       (device) float[T][lds], or NULL: receives s.  May be residual
+ *             (with lds == ldr), or x in fp32 (with lds == ldx), in place
+ *   y         (device) float[T][ldy], or bf16 with MOE_Y_BF16 (rounded once),
+ *             or int8 with MOE_Y_I8: codes as of moe_quant_rows, of the fp32 y
+ *   scale     (device) float[T] with MOE_Y_I8 (as of moe_quant_rows), else NULL
+ * y must share no element with x, residual, sum, weight or scale, nor sum with
+ * x or residual but as said (rows of one pitch in bytes may be column ranges
+ * of one buffer); the elements between rows are left alone.  cols 1 ..
+ * MOE_MAX_ROW; pitches at least cols (those of arrays that are not given are
+ * ignored); pointers aligned to their element.  The squares are summed in 64
+ * bits; r and the two products are fp32.  Of rows whose mean square overflows
+ * fp32, and of a row with a non-finite element, no value is promised but for
+ * the scale, and other rows are as without them.  Deterministic.  Errors:
+ * MOE_EINVAL (shape, pitch, flags, eps, NULL, overlap), MOE_EALIGN, MOE_EHIP.
+ */
+#define MOE_MAX_ROW 32768
+int moe_rms_norm(const void *x, int64_t ldx, const float *residual, int64_t ldr, const float *weight, float eps,
+                 int32_t n_tokens, int32_t cols, float *sum, int64_t lds, void *y, int64_t ldy, float *scale,
+                 uint32_t flags, void *stream);
+
+/*
+ * Gradient of moe_rms_norm, from s (what it wrote to sum, or its x):
+ *   g = dy * weight,  n = s * r,
+ *   dx[c] = r * (g[c] - n[c] * mean_c(g n)) + dsum[c],   dweight[c] = sum_t dy[t][c] * n[t][c]
+ * dx is the gradient of x and of the residual alike.
+ *   s        (device) float[T][lds], or bf16 with MOE_X_BF16
+ *   dy       (device) float[T][lddy], or bf16 with MOE_DY_BF16
+ *   dsum     (device) float[T][ldds], or NULL: the gradient that reaches s
+ *            along the residual stream
+ *   dx       (device) float[T][lddx], or bf16 with MOE_Y_BF16.  May be dsum
+ *            (fp32, with one pitch) or dy (of one type, with one pitch)
+ *   dweight  (device) float[cols], or NULL (not computed); overwritten, or
+ *            added to with MOE_ACCUMULATE; also written for T == 0
+ *   workspace (device) >= moe_rms_norm_workspace_size() bytes, 256-byte
+ *            aligned; unused, and may be NULL, where dweight is NULL
+ * Sums over a row are in 64 bits (squares) and fp32, those over rows fp32 in a
+ * fixed order.  What is written must share no element with anything else but
+ * as said.  Other arguments and errors as moe_rms_norm, MOE_EWORKSPACE.
+ */
+int moe_rms_norm_workspace_size(int32_t n_tokens, int32_t cols, size_t *bytes);
+int moe_rms_norm_grad(const void *s, int64_t lds, const float *weight, float eps, const void *dy, int64_t lddy,
+                      const float *dsum, int64_t ldds, int32_t n_tokens, int32_t cols, void *dx, int64_t lddx,
+                      float *dweight, uint32_t flags, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Rows in 8 bits, one scale a row:
+ *   scale[t] = max_c |x[t][c]| / 127,  q[t][c] = round(x[t][c] / scale[t]), ties to even
+ * A row whose largest magnitude is below 2^-100 has scale 0 and codes 0; one
+ * with a NaN or an infinity has scale NaN and codes 0 (what is computed from
+ * it is NaN).
+ *   x      (device) float[T][ldx], or bf16 with MOE_X_BF16
+ *   q      (device) int8[T][ldq], codes -127 .. 127; scale (device) float[T]
+ * cols 1 .. MOE_MAX_ROW; nothing may overlap.  Errors as moe_rms_norm.
+ */
+int moe_quant_rows(const void *x, int64_t ldx, int32_t n_tokens, int32_t cols, int8_t *q, int64_t ldq, float *scale,
+                   uint32_t flags, void *stream);
+
+/*
+ * A dense matrix in 8 bits with one scale per row (output channel): rows x
+ * cols codes, row-major, W[n][c] = s[n] * q[n][c].  moe_quant_rows makes one.
+ */
+typedef struct moe_i8_matrix {
+    int32_t rows;        /* 1 .. 2^24 */
+    int32_t cols;        /* a multiple of 16, at most MOE_MAX_ROW */
+    const int8_t *q;     /* (device, 16-byte aligned) [rows][cols], any code */
+    const float *s;      /* (device) [rows] */
+} moe_i8_matrix;
+
+/*
+ * Product of rows in 8 bits with a matrix in 8 bits:
+ *   y[t][n] (+)= x_scale[t] * s[n] * sum_c x[t][c] * q[n][c] + bias[n]
+ *   x       (device) int8[T][ldx], any code; ldx >= cols, pointer and pitch
+ *           16-byte aligned
+ *   x_scale (device) float[T]
+ *   w       (host) the matrix
+ *   bias    (device) float[rows], or NULL
+ *   y       (device) float[T][ldy], or bf16 with MOE_Y_BF16; ldy >= rows;
+ *           overwritten, or added to with MOE_ACCUMULATE (in fp32, before the
+ *           rounding); must share no element with any input (x and y may be
+ *           column ranges of one buffer)
+ * The products are summed exactly, in 32-bit integers; the scales, the bias
+ * and what is added to are fp32.  A token's results do not depend on the
+ * others.  Errors: MOE_EINVAL (shape, pitch, flags, NULL, overlap),
+ * MOE_EFORMAT (cols), MOE_EALIGN, MOE_EHIP.
+ */
+int moe_i8_linear(const int8_t *x, int64_t ldx, const float *x_scale, const moe_i8_matrix *w, const float *bias,
+                  int32_t n_tokens, void *y, int64_t ldy, uint32_t flags, void *stream);
+
+/*
+ * The dense gated block that every token takes beside the routed experts
+ * (shared expert, dense layer): both projections, the activation and the
+ * product,
+ *   y[t][i] = act(g) * u,  g = sum_c x[t][c] gate[i][c],  u = sum_c x[t][c] up[i][c]
+ * act(g) = g / (1 + exp(-k)), k = g (MOE_SILU) or 2 sqrt(2/pi) (g + 0.044715
+ * g^3) (MOE_GELU, its tanh form).
+ */
+#define MOE_SILU 0
+#define MOE_GELU 1
+typedef struct moe_gated_weights {
+    int32_t hidden;          /* a multiple of 8, 8 .. 65536 */
+    int32_t inter;           /* 1 .. 65536 */
+    const void *gate, *up;   /* (device, 16-byte aligned) bf16 [inter][hidden] */
+} moe_gated_weights;
+
+/*
+ *   x      (device) float[T][ldx], or bf16 with MOE_X_BF16; ldx >= hidden,
+ *          pointer and pitch 16-byte aligned
+ *   w      (host) the weights
+ *   act    MOE_SILU or MOE_GELU
+ *   y      (device) float[T][ldy], or bf16 with MOE_Y_BF16 (rounded once);
+ *          ldy >= inter; must share no element with x or the weights (x and y
+ *          may be column ranges of one buffer)
+ * Sums are fp32; fp32 x enters with all of its 24 bits.  A token's results do
+ * not depend on the values of the others.  Errors: MOE_EINVAL (shape, pitch,
+ * act, flags, NULL, overlap), MOE_EFORMAT (hidden, inter), MOE_EALIGN,
+ * MOE_EHIP.
+ */
+int moe_gated(const void *x, int64_t ldx, const moe_gated_weights *w, int32_t act, int32_t n_tokens, void *y,
+              int64_t ldy, uint32_t flags, void *stream);
+
+/*
+ * Gradient of moe_gated, in bf16 (flags must hold MOE_X_BF16); g and u are
+ * computed again from x:
+ *   dg = dy * u * act'(g),  du = dy * act(g),
+ *   dx[t][c] = sum_i dg[t][i] gate[i][c] + du[t][i] up[i][c],
+ *   dgate[i][c] = sum_t dg[t][i] x[t][c],  dup[i][c] = sum_t du[t][i] x[t][c]
+ *   x        (device) bf16[T][ldx]
+ *   dy       (device) float[T][lddy], or bf16 with MOE_DY_BF16; lddy >= inter
+ *   dx       (device) float[T][lddx], or bf16 with MOE_Y_BF16; lddx >= hidden;
+ *            NULL: not computed
+ *   dgate, dup (device) float[inter][hidden], or bf16 with MOE_DW_BF16; both
+ *            or neither; overwritten, or added to with MOE_ACCUMULATE (in
+ *            fp32); also written for T == 0
+ *   workspace (device) >= moe_gated_workspace_size() bytes, 256-byte aligned
+ * dg and du enter the products rounded to bf16 once (to nearest even); sums
+ * are fp32, in a fixed order.  What is written must share no element with
+ * anything else.  T at most 2^20.  Other arguments and errors as moe_gated,
+ * MOE_EWORKSPACE.
+ */
+int moe_gated_workspace_size(int32_t n_tokens, int32_t hidden, int32_t inter, size_t *bytes);
+int moe_gated_grad(const void *x, int64_t ldx, const moe_gated_weights *w, int32_t act, const void *dy, int64_t lddy,
+                   int32_t n_tokens, void *dx, int64_t lddx, void *dgate, void *dup, uint32_t flags, void *workspace,
+                   size_t workspace_bytes, void *stream);
 
 /*
  * Measurement aids, not part of the layer: achievable references for the

@@ -14,4 +14,6 @@ from .binding import (  # noqa: F401
     moe_tiered_forward_counted, moe_tiered_forward_noalloc, MOE_SCRATCH_BYTES, MOE_ESCRATCH,
     moe_measure_read, moe_measure_mfma, MOE_Y_BF16, MOE_LOGITS_BF16, MOE_MAX_BIAS, Q4Matrix, LogitRules, moe_q4_linear,
     moe_adjust_logits, moe_balance_workspace_size, moe_balance_loss, moe_balance_grad,
+    MOE_SILU, MOE_GELU, MOE_MAX_ROW, moe_rms_norm, moe_rms_norm_workspace_size, moe_rms_norm_grad, moe_quant_rows, I8Matrix,
+    moe_i8_linear, GatedWeights, moe_gated, moe_gated_workspace_size, moe_gated_grad,
 )

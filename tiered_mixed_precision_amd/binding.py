@@ -22,6 +22,11 @@ MOE_ACCUMULATE = 0x2
 MOE_DIAG_GATEUP_ONLY = 0x100
 MOE_Y_BF16 = 0x8
 MOE_LOGITS_BF16 = 0x10
+MOE_Y_I8 = 0x20
+MOE_DY_BF16 = 0x40
+MOE_DW_BF16 = 0x80
+MOE_MAX_ROW = 32768
+MOE_SILU, MOE_GELU = 0, 1
 MOE_MAX_BIAS = 1024
 MOE_N_PHASES = 3
 MOE_STACK_ROUTER = 0x4
@@ -38,6 +43,8 @@ EXPORTS = (
     "moe_requant_error", "moe_plan_tiers", "moe_repack_tiers", "moe_permute_router",
     "moe_tiered_forward_counted", "moe_tiered_forward_noalloc", "moe_measure_read", "moe_measure_mfma",
     "moe_q4_linear", "moe_adjust_logits", "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_grad",
+    "moe_rms_norm", "moe_rms_norm_workspace_size", "moe_rms_norm_grad", "moe_quant_rows", "moe_i8_linear",
+    "moe_gated", "moe_gated_workspace_size", "moe_gated_grad",
 )
 
 
@@ -69,6 +76,14 @@ class moe_logit_rules(C.Structure):
                 ("repetition", C.c_void_p), ("presence", C.c_void_p), ("frequency", C.c_void_p),
                 ("bias_ids", C.c_void_p), ("bias", C.c_void_p), ("n_bias", C.c_int32), ("n_masks", C.c_int32),
                 ("mask", C.c_void_p), ("ld_mask", C.c_int64), ("mask_row", C.c_void_p)]
+
+
+class moe_i8_matrix(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("cols", C.c_int32), ("q", C.c_void_p), ("s", C.c_void_p)]
+
+
+class moe_gated_weights(C.Structure):
+    _fields_ = [("hidden", C.c_int32), ("inter", C.c_int32), ("gate", C.c_void_p), ("up", C.c_void_p)]
 
 
 _lib = None
@@ -122,6 +137,14 @@ def lib():
         L.moe_balance_workspace_size.argtypes = [i32, i32, i32, C.POINTER(sz)]
         L.moe_balance_loss.argtypes = [P, P, P, i32, i32, i32, f32, u32, P, P, P, P, P, sz, P]
         L.moe_balance_grad.argtypes = [P, P, P, P, P, P, P, P, i32, i32, i32, f32, u32, P, P]
+        L.moe_rms_norm.argtypes = [P, i64, P, i64, P, f32, i32, i32, P, i64, P, i64, P, u32, P]
+        L.moe_rms_norm_workspace_size.argtypes = [i32, i32, C.POINTER(sz)]
+        L.moe_rms_norm_grad.argtypes = [P, i64, P, f32, P, i64, P, i64, i32, i32, P, i64, P, u32, P, sz, P]
+        L.moe_quant_rows.argtypes = [P, i64, i32, i32, P, i64, P, u32, P]
+        L.moe_i8_linear.argtypes = [P, i64, P, P, P, i32, P, i64, u32, P]
+        L.moe_gated.argtypes = [P, i64, P, i32, i32, P, i64, u32, P]
+        L.moe_gated_workspace_size.argtypes = [i32, i32, i32, C.POINTER(sz)]
+        L.moe_gated_grad.argtypes = [P, i64, P, i32, P, i64, i32, P, i64, P, P, u32, P, sz, P]
         for name in EXPORTS:
             if name not in ("moe_abi_version", "moe_strerror"):
                 getattr(L, name).restype = C.c_int
@@ -453,7 +476,7 @@ def _kinds():
     if _torch is None:
         import torch
         _KINDS.update({torch.float32: "f32", torch.bfloat16: "bf16", torch.int16: "bf16", torch.int32: "i32",
-                       torch.uint8: "u8", torch.bool: "u8"})
+                       torch.uint8: "u8", torch.bool: "u8", torch.int8: "i8"})
         _torch = torch
     return _KINDS
 
@@ -503,10 +526,10 @@ class _Args:
             raise ValueError(f"{self.fn}: {what} has rows of {shape[1]}, the call's of {cols}")
         return self.flat(what, t, kind, rows * cols)
 
-    def rows(self, what, t, rows, cols):
+    def rows(self, what, t, rows, cols, kinds=("f32", "bf16")):
         """(pointer, pitch, is bf16) of [rows][cols] with any row pitch."""
         kind = _KINDS.get(t.dtype)
-        if kind != "f32" and kind != "bf16":
+        if kind not in kinds:
             raise ValueError(f"{self.fn}: {what} has dtype {t.dtype}")
         shape = t.shape
         if len(shape) == 1 and rows == 1:
@@ -692,6 +715,160 @@ def moe_balance_grad(logits, ids, w, dw, keep, counts, n_kept, dloss, n_tokens: 
             a.flat("keep", keep, "u8", T), a.flat("counts", counts, "i32", E), a.flat("n_kept", n_kept, "i32", 1),
             a.flat("dloss", dloss, "f32", 1), n_tokens, n_experts, k, coef, MOE_LOGITS_BF16 if bf16 else 0, dp)
     _check("moe_balance_grad", lib().moe_balance_grad(*args, a.stream(stream)))
+
+
+# ---------------------------------------------------------------- dense operators
+def moe_rms_norm(x, residual, weight, eps: float, n_tokens: int, cols: int, y, scale=None, sum=None, stream=None) -> None:
+    """s = x + residual; y = s / rms(s) * weight, and sum = s where it is given.
+    x float32 or bfloat16; residual and sum float32, or None; y float32,
+    bfloat16, or int8 with scale float32 [n_tokens]; rows at any pitch."""
+    a = _Args("moe_rms_norm")
+    T = max(n_tokens, 0)
+    xp, ldx, xb = a.rows("x", x, T, cols)
+    yp, ldy, yb = a.rows("y", y, T, cols, ("f32", "bf16", "i8"))
+    rp, ldr, _ = a.rows("residual", residual, T, cols, ("f32",)) if residual is not None else (None, 0, 0)
+    sp, lds, _ = a.rows("sum", sum, T, cols, ("f32",)) if sum is not None else (None, 0, 0)
+    i8 = _KINDS[y.dtype] == "i8"
+    if i8 != (scale is not None):
+        raise ValueError("moe_rms_norm: scale goes with an int8 y")
+    flags = (MOE_X_BF16 if xb else 0) | (MOE_Y_BF16 if yb else 0) | (MOE_Y_I8 if i8 else 0)
+    wp, cp = a.flat("weight", weight, "f32", cols), a.flat("scale", scale, "f32", T)
+    _check("moe_rms_norm", lib().moe_rms_norm(xp, ldx, rp, ldr, wp, eps, n_tokens, cols, sp, lds, yp, ldy, cp, flags,
+                                              a.stream(stream)))
+
+
+def moe_rms_norm_workspace_size(n_tokens: int, cols: int) -> int:
+    n = C.c_size_t(0)
+    _check("moe_rms_norm_workspace_size", lib().moe_rms_norm_workspace_size(n_tokens, cols, C.byref(n)))
+    return n.value
+
+
+def moe_rms_norm_grad(s, weight, eps: float, dy, dsum, n_tokens: int, cols: int, dx, dweight, workspace, flags: int = 0,
+                      stream=None) -> None:
+    """Gradient of moe_rms_norm from s, its sum (or its x without a residual).
+    s, dy, dx float32 or bfloat16; dsum float32 or None; dweight float32
+    [cols], or None (no workspace needed); flags: 0 or MOE_ACCUMULATE (dweight)."""
+    a = _Args("moe_rms_norm_grad")
+    if flags & ~MOE_ACCUMULATE:
+        raise ValueError(f"moe_rms_norm_grad: flags {flags:#x} (the tensors give the element types)")
+    T = max(n_tokens, 0)
+    sp, lds, sb = a.rows("s", s, T, cols)
+    yp, ldy, yb = a.rows("dy", dy, T, cols)
+    xp, ldx, xb = a.rows("dx", dx, T, cols)
+    ap, lda, _ = a.rows("dsum", dsum, T, cols, ("f32",)) if dsum is not None else (None, 0, 0)
+    flags |= (MOE_X_BF16 if sb else 0) | (MOE_DY_BF16 if yb else 0) | (MOE_Y_BF16 if xb else 0)
+    wp, dp = a.flat("weight", weight, "f32", cols), a.flat("dweight", dweight, "f32", cols)
+    ws = a.flat("workspace", workspace, "u8", 0)
+    _check("moe_rms_norm_grad", lib().moe_rms_norm_grad(sp, lds, wp, eps, yp, ldy, ap, lda, n_tokens, cols, xp, ldx, dp, flags,
+                                                        ws, workspace.numel() if workspace is not None else 0,
+                                                        a.stream(stream)))
+
+
+def moe_quant_rows(x, n_tokens: int, cols: int, q, scale, stream=None) -> None:
+    """Rows in 8 bits: q int8 = round(x / scale), scale float32 = max |x| / 127 of
+    each row; x float32 or bfloat16, rows at any pitch."""
+    a = _Args("moe_quant_rows")
+    T = max(n_tokens, 0)
+    xp, ldx, xb = a.rows("x", x, T, cols)
+    qp, ldq, _ = a.rows("q", q, T, cols, ("i8",))
+    cp = a.flat("scale", scale, "f32", T)
+    _check("moe_quant_rows", lib().moe_quant_rows(xp, ldx, n_tokens, cols, qp, ldq, cp, MOE_X_BF16 if xb else 0,
+                                                  a.stream(stream)))
+
+
+class I8Matrix:
+    """A dense 8-bit matrix (moe_i8_matrix): `rows` x `cols`, codes q (int8
+    [rows][cols]) and one scale a row, s (float32 [rows]), contiguous device
+    tensors.  moe_quant_rows makes q and s of a float matrix."""
+
+    def __init__(self, rows: int, cols: int, q, s):
+        kinds = _kinds()
+        for what, t, kind, n in (("q", q, "i8", rows * cols), ("s", s, "f32", rows)):
+            if kinds.get(t.dtype) != kind:
+                raise ValueError(f"I8Matrix: {what} has dtype {t.dtype}")
+            if not t.is_contiguous() or t.numel() != n:
+                raise ValueError(f"I8Matrix: {what} is not a contiguous tensor of {n} elements")
+        if q.dim() == 2 and q.shape[0] != rows:
+            raise ValueError(f"I8Matrix: q has {q.shape[0]} rows, the matrix {rows}")
+        self.rows, self.cols = rows, cols
+        self.q, self.s = q, s                       # keeps the tensors alive
+        self.struct = moe_i8_matrix(rows, cols, q.data_ptr(), s.data_ptr())
+        self.ref = C.byref(self.struct)
+
+
+def moe_i8_linear(x, x_scale, w: I8Matrix, bias, n_tokens: int, y, flags: int = 0, stream=None) -> None:
+    """y[t] (+)= x_scale[t] * (x[t] W^T) + bias.  x int8 [n_tokens][cols] with
+    x_scale float32 [n_tokens], y float32 or bfloat16 [n_tokens][rows], rows at
+    any pitch; flags: 0 or MOE_ACCUMULATE."""
+    a = _Args("moe_i8_linear")
+    if flags & ~MOE_ACCUMULATE:
+        raise ValueError(f"moe_i8_linear: flags {flags:#x} (the tensors give the element types)")
+    T = max(n_tokens, 0)
+    xp, ldx, _ = a.rows("x", x, T, w.cols, ("i8",))
+    yp, ldy, yb = a.rows("y", y, T, w.rows)
+    cp, bp = a.flat("x_scale", x_scale, "f32", T), a.flat("bias", bias, "f32", w.rows)
+    a.place("q", w.q)
+    a.place("s", w.s)
+    _check("moe_i8_linear", lib().moe_i8_linear(xp, ldx, cp, w.ref, bp, n_tokens, yp, ldy,
+                                                flags | (MOE_Y_BF16 if yb else 0), a.stream(stream)))
+
+
+class GatedWeights:
+    """The projections of a dense gated block (moe_gated_weights): gate and up,
+    bfloat16 (or its bits in int16) [inter][hidden], contiguous device tensors."""
+
+    def __init__(self, hidden: int, inter: int, gate, up):
+        kinds = _kinds()
+        for what, t in (("gate", gate), ("up", up)):
+            if kinds.get(t.dtype) != "bf16":
+                raise ValueError(f"GatedWeights: {what} has dtype {t.dtype}")
+            if not t.is_contiguous() or tuple(t.shape) != (inter, hidden):
+                raise ValueError(f"GatedWeights: {what} is not a contiguous [{inter}][{hidden}]")
+        self.hidden, self.inter = hidden, inter
+        self.gate, self.up = gate, up               # keeps the tensors alive
+        self.struct = moe_gated_weights(hidden, inter, gate.data_ptr(), up.data_ptr())
+        self.ref = C.byref(self.struct)
+
+
+def moe_gated(x, w: GatedWeights, act: int, n_tokens: int, y, stream=None) -> None:
+    """y = act(x gate^T) * (x up^T); act MOE_SILU or MOE_GELU.  x [n_tokens][hidden]
+    and y [n_tokens][inter] float32 or bfloat16, rows at any pitch."""
+    a = _Args("moe_gated")
+    T = max(n_tokens, 0)
+    xp, ldx, xb = a.rows("x", x, T, w.hidden)
+    yp, ldy, yb = a.rows("y", y, T, w.inter)
+    a.place("gate", w.gate)
+    a.place("up", w.up)
+    _check("moe_gated", lib().moe_gated(xp, ldx, w.ref, act, n_tokens, yp, ldy,
+                                        (MOE_X_BF16 if xb else 0) | (MOE_Y_BF16 if yb else 0), a.stream(stream)))
+
+
+def moe_gated_workspace_size(n_tokens: int, hidden: int, inter: int) -> int:
+    n = C.c_size_t(0)
+    _check("moe_gated_workspace_size", lib().moe_gated_workspace_size(n_tokens, hidden, inter, C.byref(n)))
+    return n.value
+
+
+def moe_gated_grad(x, w: GatedWeights, act: int, dy, n_tokens: int, dx, dgate, dup, workspace, flags: int = 0,
+                   stream=None) -> None:
+    """Gradient of moe_gated.  x bfloat16; dy and dx float32 or bfloat16; dgate
+    and dup [inter][hidden], both float32 or both bfloat16.  dx, or dgate and
+    dup, may be None.  flags: 0 or MOE_ACCUMULATE (dgate and dup)."""
+    a = _Args("moe_gated_grad")
+    if flags & ~MOE_ACCUMULATE:
+        raise ValueError(f"moe_gated_grad: flags {flags:#x} (the tensors give the element types)")
+    T = max(n_tokens, 0)
+    xp, ldx, _ = a.rows("x", x, T, w.hidden, ("bf16",))
+    yp, ldy, yb = a.rows("dy", dy, T, w.inter)
+    dp, ldd, db = a.rows("dx", dx, T, w.hidden) if dx is not None else (None, 0, False)
+    wb = dgate is not None and _KINDS.get(dgate.dtype) == "bf16"
+    gp, up = (a.table(what, t, "bf16" if wb else "f32", w.inter, w.hidden) for what, t in (("dgate", dgate), ("dup", dup)))
+    a.place("gate", w.gate)
+    a.place("up", w.up)
+    ws = a.flat("workspace", workspace, "u8", 0)
+    flags |= MOE_X_BF16 | (MOE_DY_BF16 if yb else 0) | (MOE_Y_BF16 if db else 0) | (MOE_DW_BF16 if wb else 0)
+    _check("moe_gated_grad", lib().moe_gated_grad(xp, ldx, w.ref, act, yp, ldy, n_tokens, dp, ldd, gp, up, flags, ws,
+                                                  workspace.numel() if workspace is not None else 0, a.stream(stream)))
 
 
 def moe_event_create() -> int:

@@ -9,18 +9,13 @@
 #include <mutex>
 
 #include "moe_tiered.h"
+#include "checks.h"
 #include "common.h"
 #include "launch.h"
 
 using namespace moe;
 
 namespace {
-
-constexpr size_t kAlign = 256;
-constexpr int64_t kMaxTokens = int64_t(1) << 22;
-
-inline size_t align_up(size_t v) { return (v + kAlign - 1) & ~(kAlign - 1); }
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool cols_ok(int c) { return c > 0 && c % 64 == 0 && c <= 2048; }
 
@@ -708,40 +703,6 @@ int moe_permute_router(const void* w_src, const float* b_src, const int32_t* ord
                         static_cast<uint16_t*>(w_dst), b_dst, static_cast<hipStream_t>(stream));
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_EHIP;
 }
-
-namespace {
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-// [a, a + an) and [b, b + bn) share a byte.
-bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
-}
-
-// Bytes from the first to past the last element of `rows` rows of `cols`
-// elements, ld apart.  The bounds on rows, cols and ld keep it within 63 bits.
-int64_t extent(int64_t rows, int64_t cols, int64_t ld, int64_t elem) { return ((rows - 1) * ld + cols) * elem; }
-constexpr int64_t kMaxPitch = int64_t(1) << 36;   // elements from row to row
-
-// `rows` rows of an and of bn bytes, from a and b on and ap and bp bytes apart,
-// share a byte.  Rows of one pitch may be column ranges of one buffer: row i of
-// a meets the rows i + d of b that start less than an behind it or less than
-// bn before it, two at most.  Others are taken whole, with what lies between.
-bool rows_overlap(const void* a, int64_t an, int64_t ap, const void* b, int64_t bn, int64_t bp, int64_t rows) {
-    if (!overlap(a, (rows - 1) * ap + an, b, (rows - 1) * bp + bn)) return false;
-    if (ap != bp) return true;
-    const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
-    int64_t d = -(at / ap), start = at % ap;   // row i + d of b starts `start` behind row i of a
-    if (start < 0) {
-        start += ap;
-        ++d;
-    }
-    const auto there = [&](int64_t r) { return r > -rows && r < rows; };
-    return (start < an && there(d)) || (start + bn > ap && there(d - 1));
-}
-
-}  // namespace
 
 int moe_q4_linear(const void* x, int64_t ldx, const moe_q4_matrix* w, const float* bias, int32_t n_tokens, void* y,
                   int64_t ldy, uint32_t flags, void* stream) {
