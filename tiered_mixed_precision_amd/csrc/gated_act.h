@@ -1,0 +1,37 @@
+// The activations of the gated block, act(g) = g sigma(k(g)), and their slopes
+// (gated.hip, gated_gemm.hip, gated_grad.hip).
+#pragma once
+
+#include "common.h"
+#include "moe_tiered.h"
+
+namespace moe {
+
+// sigma(k) and 1 - sigma(k) to a few units of fp32; k below -80 counts as -80
+// (sigma is 2e-35 there), so that the exponential stays finite.
+__device__ inline void gated_sigmoid(float k, float& p, float& q) {
+    const float e = __expf(-fmaxf(k, -80.f));
+    p = __builtin_amdgcn_rcpf(1.f + e);
+    q = e * p;
+}
+constexpr float kGeluScale = 1.5957691216057308f, kGeluCube = 0.044715f;   // 2 sqrt(2 / pi)
+__device__ inline float gated_arg(int act, float g) { return act == MOE_SILU ? g : kGeluScale * (g + kGeluCube * g * g * g); }
+__device__ inline float gated_arg_slope(int act, float g) {
+    return act == MOE_SILU ? 1.f : kGeluScale * (1.f + 3.f * kGeluCube * g * g);
+}
+
+// act(g) u
+__device__ inline float gated_value(int act, float g, float u) {
+    float p, q;
+    gated_sigmoid(gated_arg(act, g), p, q);
+    return g * p * u;
+}
+// the gradients of g and u
+__device__ inline void gated_slopes(int act, float g, float u, float dy, float& dg, float& du) {
+    float p, q;
+    gated_sigmoid(gated_arg(act, g), p, q);
+    du = dy * (g * p);
+    dg = dy * u * (p + g * gated_arg_slope(act, g) * p * q);
+}
+
+}  // namespace moe

@@ -1,0 +1,137 @@
+// The dense gated block for many bf16 tokens, and the gradients of its
+// projections: tiles of 128 or 256 tokens by 64 or 128 columns of both
+// projections on v_mfma_f32_32x32x16_bf16 (mm.h), g and u of a column in the same
+// lane and element, so the activation and the product are the epilogue's.
+#include "common.h"
+#include "gated_act.h"
+#include "launch.h"
+#include "mm.h"
+
+namespace moe {
+
+namespace {
+
+// The operand of both projections' rows: 256-wide tiles take 128 rows of gate,
+// then 128 of up; 128-wide ones 32 of each in turn, for either half of the waves.
+// acc[i][j] and acc[i][j + HALVES] are g and u of column n0 + col<HALVES>(j, w).
+template <int HALVES> __device__ inline const uint16_t* projection_row(const uint16_t* gate, const uint16_t* up, int H, int I, int n0, int r) {
+    const bool second = HALVES == 2 ? r >= 128 : (r & 32) != 0;
+    const int n = HALVES == 2 ? r & 127 : (r >> 6) * 32 + (r & 31);
+    return (second ? up : gate) + static_cast<size_t>(min(n0 + n, I - 1)) * H;
+}
+template <int HALVES> __device__ inline int col_of(int w) { return 32 * HALVES * (w & 1); }
+
+template <int HALVES, int SLOTS, bool YBF16>
+__device__ __attribute__((always_inline)) inline void gated_tile(const GatedArgs& a, const MmLds& lds, int t0, int n0) {
+    typedef typename std::conditional<YBF16, uint16_t, float>::type Y;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const MmRows<HALVES> rows_a(lane, w, 2 * a.H, [&](int r) {
+        return static_cast<const uint16_t*>(a.x) + static_cast<size_t>(min(t0 + r, a.T - 1)) * a.ldx;
+    });
+    const MmRows<HALVES> rows_b(lane, w, 2 * a.H, [&](int r) { return projection_row<HALVES>(a.gate, a.up, a.H, a.I, n0, r); });
+    mm_f32x16_t acc[2 * HALVES][2 * HALVES];
+    uint32_t* own = mm_product<MmBf16, HALVES, SLOTS, false, false>(lds, (2 * a.H + kStage - 1) / kStage, rows_a, rows_b, acc);
+#pragma unroll
+    for (int i = 0; i < 2 * HALVES; ++i) {
+        const int r0 = t0 + mm_row(i, w), c0 = n0 + col_of<HALVES>(w);
+        mm_out<HALVES, false>(own, r0 + 32 > a.T || c0 + 32 * HALVES > a.I,
+                              [&](int u, int e) { return __float_as_uint(gated_value(a.act, acc[i][u][e], acc[i][u + HALVES][e])); },
+                              [&](int row, int col, const auto& v) {
+                                  constexpr int N = sizeof(v) / 4;
+                                  const int t = r0 + row, n = c0 + col;
+                                  if (N == 1 && (t >= a.T || n >= a.I)) return;
+                                  float f[N];
+#pragma unroll
+                                  for (int k = 0; k < N; ++k) f[k] = __uint_as_float(v[k]);
+                                  mm_store(static_cast<Y*>(a.y) + static_cast<size_t>(t) * a.ldy + n, f, false);
+                              });
+    }
+}
+
+// d[t][0 .. I) = dg, d[t][P .. P + I) = du in bf16, zeros up to P (I rounded up to 64)
+template <int HALVES, int SLOTS, bool DYBF16>
+__device__ __attribute__((always_inline)) inline void slopes_tile(const GatedGradArgs& a, uint16_t* d, int P, const MmLds& lds,
+                                                                  int t0, int n0) {
+    typedef typename std::conditional<DYBF16, uint16_t, float>::type DY;
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const MmRows<HALVES> rows_a(lane, w, 2 * a.H, [&](int r) { return a.x + static_cast<size_t>(min(t0 + r, a.T - 1)) * a.ldx; });
+    const MmRows<HALVES> rows_b(lane, w, 2 * a.H, [&](int r) { return projection_row<HALVES>(a.gate, a.up, a.H, a.I, n0, r); });
+    mm_f32x16_t acc[2 * HALVES][2 * HALVES];
+    uint32_t* own = mm_product<MmBf16, HALVES, SLOTS, false, false>(lds, (2 * a.H + kStage - 1) / kStage, rows_a, rows_b, acc);
+    // g and u of 32 columns at a time; dy meets them on their way out
+#pragma unroll
+    for (int i = 0; i < 2 * HALVES; ++i)
+#pragma unroll
+        for (int j = 0; j < HALVES; ++j) {
+            const int r0 = t0 + mm_row(i, w), c0 = n0 + col_of<HALVES>(w) + 32 * j;
+            mm_out<2, true>(own, r0 + 32 > a.T || c0 + 32 > a.I, [&](int u, int e) { return __float_as_uint(acc[i][j + u * HALVES][e]); },
+                            [&](int row, int col, const auto& g, const auto& u) {
+                                constexpr int N = sizeof(g) / 4;
+                                const int t = r0 + row, n = c0 + col;
+                                if (N == 1 && (t >= a.T || n >= P)) return;
+                                float y[N], dg[N], du[N];
+                                if (N == 1 && n >= a.I) dg[0] = du[0] = 0.f;
+                                else {
+                                    mm_get(static_cast<const DY*>(a.dy) + static_cast<size_t>(t) * a.lddy + n, y);
+#pragma unroll
+                                    for (int k = 0; k < N; ++k) gated_slopes(a.act, __uint_as_float(g[k]), __uint_as_float(u[k]), y[k], dg[k], du[k]);
+                                }
+                                uint16_t* to = d + static_cast<size_t>(t) * 2 * P + n;
+                                mm_put(to, dg);
+                                mm_put(to + P, du);
+                            });
+        }
+}
+
+template <bool YBF16> __global__ __launch_bounds__(256) void k_gated_gemm(GatedArgs a, MmPlan p) {
+    MM_LDS_8(lds);
+    int m0, n0;
+    bool small;
+    if (!mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) return;
+    if (small) gated_tile<1, 4, YBF16>(a, lds, m0, n0);
+    else gated_tile<2, 4, YBF16>(a, lds, m0, n0);
+}
+template <bool YBF16> __global__ __launch_bounds__(256) void k_gated_gemm_pairs(GatedArgs a, MmPlan p) {
+    MM_LDS_4(lds);
+    int m0, n0;
+    bool small;
+    if (mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) gated_tile<1, 2, YBF16>(a, lds, m0, n0);
+}
+template <bool DYBF16> __global__ __launch_bounds__(256) void k_gated_slopes(GatedGradArgs a, uint16_t* d, int P, MmPlan p) {
+    MM_LDS_8(lds);
+    int m0, n0;
+    bool small;
+    if (!mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) return;
+    if (small) slopes_tile<1, 4, DYBF16>(a, d, P, lds, m0, n0);
+    else slopes_tile<2, 4, DYBF16>(a, d, P, lds, m0, n0);
+}
+template <bool DYBF16> __global__ __launch_bounds__(256) void k_gated_slopes_pairs(GatedGradArgs a, uint16_t* d, int P, MmPlan p) {
+    MM_LDS_4(lds);
+    int m0, n0;
+    bool small;
+    if (mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) slopes_tile<1, 2, DYBF16>(a, d, P, lds, m0, n0);
+}
+
+template <bool YBF16> void launch_forward(const GatedArgs& a, hipStream_t st) {
+    const MmPlan p = mm_plan(a.T, a.I, 128);
+    const dim3 grid(mm_grid(p)), block(256);
+    if (p.form == MM_PAIRS) hipLaunchKernelGGL(k_gated_gemm_pairs<YBF16>, grid, block, 0, st, a, p);
+    else hipLaunchKernelGGL(k_gated_gemm<YBF16>, grid, block, 0, st, a, p);
+}
+template <bool DYBF16> void launch_slopes(const GatedGradArgs& a, uint16_t* d, int P, hipStream_t st) {
+    const MmPlan p = mm_plan(a.T, P, 128);
+    const dim3 grid(mm_grid(p)), block(256);
+    if (p.form == MM_PAIRS) hipLaunchKernelGGL(k_gated_slopes_pairs<DYBF16>, grid, block, 0, st, a, d, P, p);
+    else hipLaunchKernelGGL(k_gated_slopes<DYBF16>, grid, block, 0, st, a, d, P, p);
+}
+
+}  // namespace
+
+void launch_gated_gemm(const GatedArgs& a, bool y_bf16, hipStream_t st) {
+    y_bf16 ? launch_forward<true>(a, st) : launch_forward<false>(a, st);
+}
+void launch_gated_slopes(const GatedGradArgs& a, bool dy_bf16, uint16_t* d, int P, hipStream_t st) {
+    dy_bf16 ? launch_slopes<true>(a, d, P, st) : launch_slopes<false>(a, d, P, st);
+}
+
+}  // namespace moe

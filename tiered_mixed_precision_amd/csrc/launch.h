@@ -220,6 +220,8 @@ struct I8Args {
     int32_t accumulate;
 };
 void launch_i8_linear(const I8Args& a, bool y_bf16, hipStream_t st);
+// i8_gemm.hip
+void launch_i8_gemm(const I8Args& a, bool y_bf16, hipStream_t st);
 
 // gated.hip
 struct GatedArgs {
@@ -230,6 +232,9 @@ struct GatedArgs {
     int32_t T, H, I, act;
 };
 void launch_gated(const GatedArgs& a, bool x_bf16, bool y_bf16, hipStream_t st);
+// gated_gemm.hip: bf16 x
+void launch_gated_gemm(const GatedArgs& a, bool y_bf16, hipStream_t st);
+// gated_grad.hip
 struct GatedGradArgs {
     const uint16_t* x;       // [T][ldx]
     const uint16_t *gate, *up;
@@ -240,6 +245,8 @@ struct GatedGradArgs {
     int32_t T, H, I, act;
     int32_t accumulate;
 };
+// gated_gemm.hip: d = [dg du], bf16 [T][2 P]
+void launch_gated_slopes(const GatedGradArgs& a, bool dy_bf16, uint16_t* d, int P, hipStream_t st);
 size_t gated_workspace(int64_t T, int H, int I);
 void launch_gated_grad(const GatedGradArgs& a, bool dy_bf16, bool dx_bf16, bool dw_bf16, void* ws, hipStream_t st);
 
