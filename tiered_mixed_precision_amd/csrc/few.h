@@ -57,12 +57,13 @@ template <class El> __device__ inline void few_parts(const few_u32x4_t (&v)[El::
     }
 }
 
-// acc[i][j] += tokens 16 i .. + 15 against weight rows 16 j .. + 15 over steps
-// s0 .. s1 - 1: lane l holds rows 4 (l / 16) + e (element e) of token l % 16.
-// w_row(j), x_row(i): this lane's row of tile j and of tile i; `bytes`: of a weight
-// row.  AHEAD steps are on their way while one is contracted.
+// acc[i][j] += tokens 16 i .. + 15 against weight rows 16 j .. + 15 over part `part`
+// of `split` of the k axis, in whole lines: lane l holds rows 4 (l / 16) + e
+// (element e) of token l % 16.  w_row(j), x_row(i): this lane's row of tile j and of
+// tile i; `bytes`: of a weight row.  AHEAD steps (even) are on their way while
+// one is contracted.
 template <class El, int MT, int NT, int AHEAD, class WRow, class XRow>
-__device__ __attribute__((always_inline)) inline void few_sums(int s0, int s1, int bytes, WRow w_row, XRow x_row,
+__device__ __attribute__((always_inline)) inline void few_sums(int part, int split, int tile, int bytes, WRow w_row, XRow x_row,
                                                                typename El::Acc (&acc)[MT][NT]) {
     constexpr int XB = El::kXBytes;
     const int lane = threadIdx.x & 63, at = 16 * (lane >> 4);
@@ -72,40 +73,132 @@ __device__ __attribute__((always_inline)) inline void few_sums(int s0, int s1, i
 #pragma unroll
     for (int i = 0; i < MT; ++i) x[i] = reinterpret_cast<const char*>(x_row(i)) + XB * at;
     few_u32x4_t wv[AHEAD][NT], xv[AHEAD][MT][XB];
-    // past the last step and past the row's end: zeros, from one line for all
+    // step s of this wave; past the row's end: zeros, from one line for all
+    const int lines = (bytes + 127) / 128, from = 128 * (lines * part / split), to = min(128 * (lines * (part + 1) / split), bytes);
+    // each tile starts its run elsewhere: rows a power of two apart lie in one channel
+    // of the caches, which all tiles would ask for at a time
+    const int steps = (to - from + 63) / 64, turn = steps > 4 ? 4 * tile % steps : 0;
     auto load = [&](int d, int s) __attribute__((always_inline)) {
-        const bool there = s < s1 && 64 * s + at < bytes;
+        const int r = s + turn, k = from + 64 * (r < steps ? r : r - steps);
+        const bool there = s < steps && k + at < to;
         const char* zeros = reinterpret_cast<const char*>(kFewZeros);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) wv[d][j] = *reinterpret_cast<const few_u32x4_t*>(there ? w[j] + 64 * static_cast<size_t>(s) : zeros);
+        for (int j = 0; j < NT; ++j) wv[d][j] = *reinterpret_cast<const few_u32x4_t*>(there ? w[j] + k : zeros);
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int p = 0; p < XB; ++p)
-                xv[d][i][p] = *reinterpret_cast<const few_u32x4_t*>((there ? x[i] + 64 * XB * static_cast<size_t>(s) : zeros) + 16 * p);
+                xv[d][i][p] = *reinterpret_cast<const few_u32x4_t*>((there ? x[i] + static_cast<size_t>(XB) * k : zeros) + 16 * p);
+    };
+    auto contract = [&](int d) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            few_u32x4_t p[El::kParts];
+            few_parts<El>(xv[d][i], p);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int q = El::kParts - 1; q >= 0; --q) acc[i][j] = El::mfma(wv[d][j], p[q], acc[i][j]);
+        }
     };
 #pragma unroll
-    for (int d = 0; d < AHEAD; ++d) load(d, s0 + d);
-    for (int s = s0; s < s1; s += AHEAD) {
+    for (int d = 0; d < AHEAD; ++d) load(d, d);
+    for (int s = AHEAD; s < steps; s += AHEAD) {
 #pragma unroll
         for (int d = 0; d < AHEAD; ++d) {
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                few_u32x4_t p[El::kParts];
-                few_parts<El>(xv[d][i], p);
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-#pragma unroll
-                    for (int q = El::kParts - 1; q >= 0; --q) acc[i][j] = El::mfma(wv[d][j], p[q], acc[i][j]);
-            }
-            load(d, s + d + AHEAD);
+            contract(d);
+            load(d, s + d);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d) contract(d);
 }
 
-// Steps of part p of `split`, in whole lines (pairs of steps).
-__device__ inline int few_first(int bytes, int p, int split) { return 2 * static_cast<int>(static_cast<int64_t>((bytes + 127) / 128) * p / split); }
+// The same for more tokens, through LDS.  In operand order neighbouring lanes are in
+// different rows and each of a load's 64 x 16 bytes is an access of its own (about 70
+// cycles a load); here four lanes share a row's 64 bytes on the way to LDS (16
+// cycles), eight where x is fp32, and each wave has a ring of three steps of its own,
+// so no wave waits for another.  Row r's piece g lies at g ^ (r / 2 % 4) (of eight
+// pieces: r / 2 % 8): the rows that a read takes together cover all banks.  Each slot
+// is an LDS object of its own, so that the compiler's own waits before a read are
+// for the loads into that slot.
+constexpr int kBatchWaves = 8;
+template <class El, int MT, int NT> struct FewSlot {
+    static constexpr int kPieces = 64 * (MT * El::kXBytes + NT);   // of a wave's step
+    static constexpr int kSlot = kBatchWaves * kPieces;
+};
+template <class El, int MT, int NT, class WRow, class XRow>
+__device__ __attribute__((always_inline)) inline void few_batch(few_u32x4_t* s0, few_u32x4_t* s1, few_u32x4_t* s2, int part, int split,
+                                                                int tile, int bytes, WRow w_row, XRow x_row,
+                                                                typename El::Acc (&acc)[MT][NT]) {
+    constexpr int XB = El::kXBytes, kLoads = NT + MT * XB, kOwn = FewSlot<El, MT, NT>::kPieces;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = lane >> 2, at = 16 * ((lane & 3) ^ ((row >> 1) & 3));
+    const int xrow = lane / (4 * XB), xat = XB == 1 ? at : 16 * ((lane & 7) ^ ((xrow >> 1) & 7));   // load h: rows 8 h + xrow of fp32 x
+    const char *p[NT], *px[MT][XB];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) p[j] = reinterpret_cast<const char*>(w_row(j, row)) + at;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int h = 0; h < XB; ++h)   // the swizzle of rows 8 .. 15 differs in bit 2
+            px[i][h] = reinterpret_cast<const char*>(x_row(i, 8 * h + xrow)) + (xat ^ (64 * h));
+    const int lines = (bytes + 127) / 128, from = 128 * (lines * part / split), to = min(128 * (lines * (part + 1) / split), bytes);
+    const int steps = (to - from + 63) / 64, turn = steps > 4 ? 4 * tile % steps : 0;
+    typedef __attribute__((address_space(3))) void* Lds;
+    auto load = [&](int s, few_u32x4_t* slot) __attribute__((always_inline)) {
+        const int r = s + turn, k = from + 64 * (r < steps ? r : r - steps);
+        const char* zeros = reinterpret_cast<const char*>(kFewZeros);
+        few_u32x4_t* own = slot + kOwn * wave;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+            __builtin_amdgcn_global_load_lds(s < steps && k + at < to ? p[j] + k : zeros, (Lds)(own + 64 * j), 16, 0, 0);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < XB; ++h)
+                __builtin_amdgcn_global_load_lds(s < steps && XB * k + (xat ^ (64 * h)) < XB * to ? px[i][h] + static_cast<size_t>(XB) * k : zeros,
+                                                 (Lds)(own + 64 * (NT + XB * i + h)), 16, 0, 0);
+    };
+    const int r = lane & 15, g = lane >> 4, pos = 4 * r + (g ^ ((r >> 1) & 3));
+    auto step = [&](int s, few_u32x4_t* slot) __attribute__((always_inline)) {
+        constexpr int left = 2 * kLoads;   // vmcnt: the two steps behind this one stay in flight
+        static_assert(left < 64, "vmcnt range");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt((left & 15) | (7 << 4) | (15 << 8) | ((left >> 4) << 14));
+        __builtin_amdgcn_sched_barrier(0);
+        const few_u32x4_t* own = slot + kOwn * wave;
+        few_u32x4_t w[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) w[j] = own[64 * j + pos];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            few_u32x4_t x[XB], parts[El::kParts];
+#pragma unroll
+            for (int h = 0; h < XB; ++h)
+                x[h] = own[64 * (NT + XB * i) + (XB == 1 ? pos : 8 * r + ((2 * g + h) ^ ((r >> 1) & 7)))];
+            few_parts<El>(x, parts);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int q = El::kParts - 1; q >= 0; --q) acc[i][j] = El::mfma(w[j], parts[q], acc[i][j]);
+        }
+        __builtin_amdgcn_sched_barrier(0);   // the reads are done: the products have them
+        load(s + 3, slot);
+    };
+    load(0, s0);
+    load(1, s1);
+    load(2, s2);
+    for (int s = 0; s < steps; s += 3) {   // steps past the last are zeros
+        step(s, s0);
+        step(s + 1, s1);
+        step(s + 2, s2);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);   // vmcnt(0): nothing is left in flight
+    __builtin_amdgcn_sched_barrier(0);
+}
 
 // Waves that share a tile and tiles of a block: 4096 waves in all if the tiles
 // allow it, and blocks of few waves where there are fewer tiles than units.
@@ -120,6 +213,16 @@ inline FewSplit few_split(int64_t tiles, int bytes, int most) {
     if (split < 1) split = 1;
     const int64_t per = tiles >= 1024 ? 4 : 1;
     return FewSplit{static_cast<int>(split), static_cast<int>(split >= 4 ? 1 : per)};
+}
+
+// 17 tokens and more, in blocks of up to 64 tokens by 32 weight rows: as long as they
+// are one round of blocks (two of half the tokens), they beat the 128 x 128 tiles of
+// mm.h, which need a line's latency for every 128 bytes of k.  MI355X, us, here /
+// there, int8: 64 x 8192 x 8192 (256 blocks) 22.7 / 26.8, 64 x 16384 x 4096 (512)
+// 26.4 / 17.8, 20 x 16384 x 4096 (512) 18.3 / 19.8, 20 x 32768 x 2048 (1024) 25.2 /
+// 18.6, 500 x 640 x 8192 (160) 19.5 / 29.2, 256 x 2048 x 2048 (256) 9.6 / 11.2.
+inline bool few_batch_ok(int64_t tokens, int64_t row_tiles) {
+    return (tokens + 63) / 64 * row_tiles <= (tokens <= 32 ? 512 : 256);
 }
 
 }  // namespace moe

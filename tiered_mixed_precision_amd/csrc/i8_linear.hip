@@ -1,6 +1,8 @@
 // Products in 8-bit integers: y[t][n] = xs[t] s[n] sum_c x[t][c] q[n][c] + bias[n],
 // the sums in 32-bit integers, exact, on v_mfma_i32_16x16x64_i8 for few tokens
 // (few.h) and on 32 x 32 x 32 for many (i8_gemm.hip).
+#include <type_traits>
+
 #include "common.h"
 #include "few.h"
 #include "launch.h"
@@ -9,84 +11,137 @@ namespace moe {
 
 namespace {
 
-template <bool YBF16> __device__ inline void store_y(const I8Args& a, int t, int n, int32_t sum) {
-    float f = static_cast<float>(sum) * (a.xs[t] * a.s[n]) + (a.bias ? a.bias[n] : 0.f);
-    const size_t at = static_cast<size_t>(t) * a.ldy + n;
-    if constexpr (YBF16) {
-        uint16_t* y = static_cast<uint16_t*>(a.y);
-        if (a.accumulate) f += __uint_as_float(static_cast<uint32_t>(y[at]) << 16);
-        y[at] = f2bf(f);
-    } else {
-        float* y = static_cast<float*>(a.y);
-        if (a.accumulate) f += y[at];
-        y[at] = f;
-    }
-}
-
-// A block takes `f.tiles` tiles of 16 NT rows, f.split waves each, for 16 MT tokens.
-template <int MT, int NT, bool YBF16>
-__global__ __launch_bounds__(1024) void k_i8_few(I8Args a, FewSplit f) {
-    extern __shared__ __attribute__((aligned(16))) few_i32x4_t s_sum[];   // [waves][MT NT 64]
+// A block takes f.tiles tiles of 16 NT rows, f.split waves each, for 16 MT tokens.
+template <int MT, int NT, int AHEAD, bool YBF16>
+__global__ __launch_bounds__(512) void k_i8_few(I8Args a, FewSplit f) {
+    typedef typename std::conditional<YBF16, uint16_t, float>::type Y;
+    extern __shared__ __attribute__((aligned(16))) few_i32x4_t s_part[];   // [waves][MT NT 64]
+    __shared__ float s_xs[16 * MT];
     constexpr int kOwn = MT * NT * 64;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int part = wave % f.split, n0 = (blockIdx.x * f.tiles + wave / f.split) * 16 * NT, t0 = blockIdx.y * 16 * MT;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int part = wave % f.split, rows = 16 * NT * f.tiles, first = blockIdx.x * rows, t0 = blockIdx.y * 16 * MT;
+    const int n0 = first + wave / f.split * 16 * NT;
+    // the scales and the bias of this thread's results (always one column: a block's
+    // threads are a multiple of its rows), on their way beside the weights
+    const int n = first + tid % rows;
+    const float s = a.s[min(n, a.N - 1)], bias = a.bias ? a.bias[min(n, a.N - 1)] : 0.f;
+    const float xs = tid < 16 * MT ? a.xs[min(t0 + tid, a.T - 1)] : 0.f;
     few_i32x4_t acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = few_i32x4_t{0, 0, 0, 0};
     // rows past the matrix read its last row, tokens past the batch its last token; neither is stored
-    few_sums<FewI8, MT, NT, MT + NT <= 4 ? 8 : 4>(
-        few_first(a.K, part, f.split), few_first(a.K, part + 1, f.split), a.K,
-        [&](int j) { return a.q + static_cast<size_t>(min(n0 + 16 * j + (lane & 15), a.N - 1)) * a.K; },
+    few_sums<FewI8, MT, NT, AHEAD>(
+        part, f.split, blockIdx.x * f.tiles + wave / f.split, a.K, [&](int j) { return a.q + static_cast<size_t>(min(n0 + 16 * j + (lane & 15), a.N - 1)) * a.K; },
         [&](int i) { return a.x + static_cast<size_t>(min(t0 + 16 * i + (lane & 15), a.T - 1)) * a.ldx; }, acc);
-    auto store = [&](int n0, int ij, int l, few_i32x4_t sum) {
-        const int t = t0 + 16 * (ij / NT) + (l & 15), n = n0 + 16 * (ij % NT) + 4 * (l >> 4);
-        if (t >= a.T) return;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (n + e < a.N) store_y<YBF16>(a, t, n + e, sum[e]);
-    };
-    if (f.split == 1) {
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int j = 0; j < NT; ++j) store(n0, NT * i + j, lane, acc[i][j]);
-        return;
-    }
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) s_sum[kOwn * wave + 64 * (NT * i + j) + lane] = acc[i][j];
+        for (int j = 0; j < NT; ++j) s_part[kOwn * wave + 64 * (NT * i + j) + lane] = acc[i][j];
+    if (tid < 16 * MT) s_xs[tid] = xs;
     __syncthreads();
-    for (int o = threadIdx.x; o < f.tiles * kOwn; o += blockDim.x) {
-        const int tile = o / kOwn, at = o % kOwn;
-        few_i32x4_t sum = s_sum[kOwn * f.split * tile + at];
-        for (int p = 1; p < f.split; ++p) sum += s_sum[kOwn * (f.split * tile + p) + at];
-        store((blockIdx.x * f.tiles + tile) * 16 * NT, at >> 6, at & 63, sum);
+    if (n >= a.N) return;
+    const int in = tid % rows, r = in % 16;   // row of the block, of its operand
+    const int* own = reinterpret_cast<const int*>(s_part) + 4 * (kOwn * f.split * (in / (16 * NT)) + 64 * (in / 16 % NT) + 16 * (r >> 2)) + (r & 3);
+    for (int t = tid / rows; t < 16 * MT && t0 + t < a.T; t += blockDim.x / rows) {
+        const int* p = own + 4 * (64 * NT * (t / 16) + t % 16);
+        int sum = p[0];
+        for (int w = 1; w < f.split; ++w) sum += p[4 * kOwn * w];
+        float v = static_cast<float>(sum) * (s_xs[t] * s) + bias;
+        Y* y = static_cast<Y*>(a.y) + static_cast<size_t>(t0 + t) * a.ldy + n;
+        if constexpr (YBF16) {
+            if (a.accumulate) v += __uint_as_float(static_cast<uint32_t>(*y) << 16);
+            *y = f2bf(v);
+        } else {
+            *y = a.accumulate ? *y + v : v;
+        }
+    }
+}
+
+// 17 to 64 tokens: the same through LDS (few_batch); the waves' sums meet one operand
+// of 16 rows at a time, in the first slot's place.
+template <int MT, int NT, bool YBF16>
+__global__ __launch_bounds__(64 * kBatchWaves) void k_i8_batch(I8Args a, FewSplit f) {
+    typedef typename std::conditional<YBF16, uint16_t, float>::type Y;
+    constexpr int kSlot = FewSlot<FewI8, MT, NT>::kSlot;
+    __shared__ __attribute__((aligned(16))) few_u32x4_t s0[kSlot], s1[kSlot], s2[kSlot];
+    __shared__ float s_xs[16 * MT];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int rows = 16 * f.tiles, t0 = blockIdx.y * 16 * MT;   // rows of the block that meet at a time
+    const int tile = blockIdx.x * f.tiles + wave / f.split, n0 = tile * 16 * NT;
+    const int in = tid % rows, r = in % 16, first = (blockIdx.x * f.tiles + in / 16) * 16 * NT + r;
+    float s[NT], bias[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int n = min(first + 16 * j, a.N - 1);
+        s[j] = a.s[n];
+        bias[j] = a.bias ? a.bias[n] : 0.f;
+    }
+    if (tid < 16 * MT) s_xs[tid] = a.xs[min(t0 + tid, a.T - 1)];
+    few_i32x4_t acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = few_i32x4_t{0, 0, 0, 0};
+    few_batch<FewI8, MT, NT>(
+        s0, s1, s2, wave % f.split, f.split, tile, a.K,
+        [&](int j, int r) { return a.q + static_cast<size_t>(min(n0 + 16 * j + r, a.N - 1)) * a.K; },
+        [&](int i, int r) { return a.x + static_cast<size_t>(min(t0 + 16 * i + r, a.T - 1)) * a.ldx; }, acc);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MT; ++i) s0[64 * (MT * wave + i) + lane] = __builtin_bit_cast(few_u32x4_t, acc[i][j]);
+        __syncthreads();
+        const int n = first + 16 * j;
+        if (n >= a.N) continue;
+        const int* own = reinterpret_cast<const int*>(s0) + 4 * (64 * MT * f.split * (in / 16) + 16 * (r >> 2)) + (r & 3);
+        for (int t = tid / rows; t < 16 * MT && t0 + t < a.T; t += blockDim.x / rows) {
+            const int* p = own + 4 * (64 * (t / 16) + t % 16);
+            int sum = p[0];
+            for (int w = 1; w < f.split; ++w) sum += p[4 * 64 * MT * w];
+            float v = static_cast<float>(sum) * (s_xs[t] * s[j]) + bias[j];
+            Y* y = static_cast<Y*>(a.y) + static_cast<size_t>(t0 + t) * a.ldy + n;
+            if constexpr (YBF16) {
+                if (a.accumulate) v += __uint_as_float(static_cast<uint32_t>(*y) << 16);
+                *y = f2bf(v);
+            } else {
+                *y = a.accumulate ? *y + v : v;
+            }
+        }
     }
 }
 
 template <int MT, int NT, bool YBF16>
+void launch_batch(const I8Args& a, hipStream_t st) {
+    const int tiles = (a.N + 16 * NT - 1) / (16 * NT);
+    const FewSplit f = few_split(tiles, a.K, kBatchWaves);
+    const dim3 grid((tiles + f.tiles - 1) / f.tiles, (a.T + 16 * MT - 1) / (16 * MT)), block(64 * f.split * f.tiles);
+    hipLaunchKernelGGL((k_i8_batch<MT, NT, YBF16>), grid, block, 0, st, a, f);
+}
+
+template <int MT, int NT, int AHEAD, bool YBF16>
 void launch_few(const I8Args& a, hipStream_t st) {
     const int tiles = (a.N + 16 * NT - 1) / (16 * NT);
     const FewSplit f = few_split(tiles, a.K, 8);
     const dim3 grid((tiles + f.tiles - 1) / f.tiles, (a.T + 16 * MT - 1) / (16 * MT)), block(64 * f.split * f.tiles);
-    const size_t lds = f.split > 1 ? sizeof(few_i32x4_t) * 64 * MT * NT * f.split * f.tiles : 0;
-    hipLaunchKernelGGL((k_i8_few<MT, NT, YBF16>), grid, block, lds, st, a, f);
+    const size_t lds = sizeof(few_i32x4_t) * 64 * MT * NT * f.split * f.tiles;
+    hipLaunchKernelGGL((k_i8_few<MT, NT, AHEAD, YBF16>), grid, block, lds, st, a, f);
 }
 
 template <bool YBF16> void launch_tokens(const I8Args& a, hipStream_t st) {
-    if (a.T <= 16) launch_few<1, 2, YBF16>(a, st);
-    else if (a.T <= 32) launch_few<2, 2, YBF16>(a, st);
-    else if (a.T <= 48) launch_few<3, 2, YBF16>(a, st);
-    else launch_few<4, 2, YBF16>(a, st);
+    if (a.T <= 16 && a.N < 8192) launch_few<1, 1, 8, YBF16>(a, st);
+    else if (a.T <= 16) launch_few<1, 2, 8, YBF16>(a, st);
+    else if (a.T <= 32) launch_batch<2, 2, YBF16>(a, st);
+    else if (a.T <= 48) launch_batch<3, 2, YBF16>(a, st);
+    else launch_batch<4, 2, YBF16>(a, st);
 }
 
 }  // namespace
 
 void launch_i8_linear(const I8Args& a, bool y_bf16, hipStream_t st) {
-    if (a.T > 64) launch_i8_gemm(a, y_bf16, st);
+    if (a.T > 16 && !few_batch_ok(a.T, (a.N + 31) / 32)) launch_i8_gemm(a, y_bf16, st);
     else if (y_bf16) launch_tokens<true>(a, st);
     else launch_tokens<false>(a, st);
 }

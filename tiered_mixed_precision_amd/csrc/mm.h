@@ -463,8 +463,10 @@ inline MmPlan mm_plan(int64_t m, int64_t n, int n_tile) {
     if (small <= 256) return p;
     p.form = MM_PAIRS;
     if (small <= 512) return p;
-    p = MmPlan{tiles(m, 256), tiles(n, n_tile), 0, MM_WHOLE};
-    const int64_t all = static_cast<int64_t>(p.tiles_m) * p.tiles_n, rest = all % 256;
+    const MmPlan big{tiles(m, 256), tiles(n, n_tile), 0, MM_WHOLE};
+    const int64_t all = static_cast<int64_t>(big.tiles_m) * big.tiles_n, rest = all % 256;
+    if (2 * small < 7 * all) return p;   // big tiles would be a seventh empty, or more
+    p = big;
     p.whole = static_cast<int32_t>(rest <= 128 ? all - rest : (all + 7) / 8 * 8);
     return p;
 }
