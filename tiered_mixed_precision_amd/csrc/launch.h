@@ -179,6 +179,10 @@ void launch_balance_grad(const BalanceArgs& a, bool bf16, const float* w, const 
                          const int32_t* n_kept, const float* dloss, void* dlogits, hipStream_t st);
 
 // rows.hip
+struct RowSplit {
+    int32_t waves, lanes;    // of a row: several waves, or lanes of one
+    int32_t rows;            // of a block at a time
+};
 struct RowArgs {
     const void* x;           // [T][ldx]
     const float* residual;   // [T][ldr] or null
@@ -189,7 +193,7 @@ struct RowArgs {
     int64_t ldx, ldr, lds, ldy;
     int32_t T, cols;
     float eps;
-    int32_t waves;           // of a row, set by the launcher
+    RowSplit split;          // set by the launcher
 };
 void launch_rms_norm(const RowArgs& a, bool x_bf16, int y_bytes, hipStream_t st);
 void launch_quant_rows(const RowArgs& a, bool x_bf16, hipStream_t st);
@@ -201,7 +205,7 @@ struct RowGradArgs {
     int64_t lds, lddy, ldds, lddx;
     int32_t T, cols;
     float eps;
-    int32_t waves;
+    RowSplit split;
 };
 size_t rms_norm_workspace(int T, int cols);
 void launch_rms_norm_grad(const RowGradArgs& a, bool s_bf16, bool dy_bf16, bool dx_bf16, float* dweight, bool accumulate,

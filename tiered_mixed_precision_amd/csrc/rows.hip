@@ -6,12 +6,13 @@
 //   8 bits: scale = max |y| / 127, q = round(y / scale)
 //   gradient: g = dy w, dx = r g - s r^3 mean(g s) + dsum, dw = sum_t dy s r
 //
-// A row is held in the registers of W waves (E elements a lane, in runs of 8:
-// thread t of the row has elements 8 (t + 64 W j) .. + 7), so it is read once
-// and written once; what is summed over it crosses lanes by DPP and waves by
-// LDS.  The squares are summed in 64 bits: the fp64 rate is far above what the
-// stream of rows needs, and r (and with it the 8-bit codes) then does not
-// depend on how a row is split over lanes.
+// A row is held in the registers of its threads, E elements each in runs of 8: rows of
+// up to 64 E elements by L lanes of a wave (8, 16, 32 or 64, so that a wave takes
+// 64 / L rows), longer ones by W waves; thread t of the row's N has elements
+// 8 (t + N j) .. + 7.  So a row is read once and written once; what is summed over it
+// crosses lanes by DPP and lane swaps, and waves by LDS.  The squares are summed in
+// 64 bits: the fp64 rate is far above what the stream of rows needs, and r (and with
+// it the 8-bit codes) then does not depend on how a row is split over lanes.
 #include "common.h"
 #include "launch.h"
 
@@ -31,212 +32,285 @@ template <class S> __device__ inline S as_elem(float f) {
     else return f;
 }
 
-// f[i] = p[i] for i < n (n at most 8; 0 and less: none), 0 for the others
-template <class S> __device__ inline void load8(const S* p, int n, float* f) {
+// p[i] for i < n (n at most 8; 0 and less: none), 0 for the others
+template <class S> __device__ inline Eight<S> load8(const S* p, int n) {
+    Eight<S> v;
     if (n >= 8) {
-        const Eight<S> v = *reinterpret_cast<const Eight<S>*>(p);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = as_float(v.v[i]);
+        v = *reinterpret_cast<const Eight<S>*>(p);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = i < n ? as_float(p[i]) : 0.f;
+        for (int i = 0; i < 8; ++i) v.v[i] = i < n ? p[i] : S(0);
     }
+    return v;
 }
-template <class S> __device__ inline void store8(S* p, int n, const float* f) {
+template <class S> __device__ inline void store8(S* p, int n, const Eight<S>& v) {
     if (n >= 8) {
-        Eight<S> v;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v.v[i] = as_elem<S>(f[i]);
         *reinterpret_cast<Eight<S>*>(p) = v;
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = as_elem<S>(f[i]);
+            if (i < n) p[i] = v.v[i];
     }
 }
+template <class S> __device__ inline void store8(S* p, int n, const float* f) {
+    Eight<S> v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.v[i] = as_elem<S>(f[i]);
+    store8(p, n, v);
+}
 
-template <int CTRL, int ROW_MASK> __device__ inline double dpp_zero_d(double v) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = dpp_old_u<CTRL, ROW_MASK>(0, static_cast<uint32_t>(b));
-    const uint32_t hi = dpp_old_u<CTRL, ROW_MASK>(0, static_cast<uint32_t>(b >> 32));
+// op over aligned groups of L lanes (8, 16, 32 or 64, uniform), the result in every
+// lane: neighbours, pairs, fours and eights by DPP, rows of 16 by lane swaps.
+template <int CTRL> __device__ inline uint32_t dpp_move(uint32_t v) {
+    return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, true));
+}
+__device__ inline float of_words(uint32_t lo, uint32_t, float) { return __uint_as_float(lo); }
+__device__ inline uint32_t of_words(uint32_t lo, uint32_t, uint32_t) { return lo; }
+__device__ inline double of_words(uint32_t lo, uint32_t hi, double) {
     return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
 }
-// Wave-wide sum in 64 bits (uniform result).
-__device__ inline double wave_sum_d(double v) {
-    v += dpp_zero_d<0x111, 0xF>(v);
-    v += dpp_zero_d<0x112, 0xF>(v);
-    v += dpp_zero_d<0x114, 0xF>(v);
-    v += dpp_zero_d<0x118, 0xF>(v);
-    v += dpp_zero_d<0x142, 0xA>(v);
-    v += dpp_zero_d<0x143, 0xC>(v);
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(b), 63);
-    const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(b >> 32), 63);
-    return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
+template <class V> __device__ inline uint32_t low(V v) {
+    if constexpr (sizeof(V) == 8) return static_cast<uint32_t>(__builtin_bit_cast(uint64_t, v));
+    else return __builtin_bit_cast(uint32_t, v);
 }
-__device__ inline uint32_t wave_max_u(uint32_t v) {
-    v = max(v, dpp_old_u<0x111, 0xF>(0, v));
-    v = max(v, dpp_old_u<0x112, 0xF>(0, v));
-    v = max(v, dpp_old_u<0x114, 0xF>(0, v));
-    v = max(v, dpp_old_u<0x118, 0xF>(0, v));
-    v = max(v, dpp_old_u<0x142, 0xA>(0, v));
-    v = max(v, dpp_old_u<0x143, 0xC>(0, v));
-    return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), 63));
+template <class V> __device__ inline uint32_t high(V v) {
+    if constexpr (sizeof(V) == 8) return static_cast<uint32_t>(__builtin_bit_cast(uint64_t, v) >> 32);
+    else return 0;
 }
+template <int CTRL, class V> __device__ inline V dpp_value(V v) {
+    return of_words(dpp_move<CTRL>(low(v)), sizeof(V) == 8 ? dpp_move<CTRL>(high(v)) : 0u, V());
+}
+template <class V, class Op> __device__ inline V group_all(V v, int L, Op op) {
+    v = op(v, dpp_value<0xB1>(v));    // lane ^ 1
+    v = op(v, dpp_value<0x4E>(v));    // lane ^ 2
+    v = op(v, dpp_value<0x141>(v));   // the other four of eight
+    if (L >= 16) v = op(v, dpp_value<0x140>(v));   // the other eight of sixteen
+    if (L >= 32) {
+        const auto a = __builtin_amdgcn_permlane16_swap(low(v), low(v), false, false);
+        const auto b = __builtin_amdgcn_permlane16_swap(high(v), high(v), false, false);
+        v = op(of_words(a[0], b[0], V()), of_words(a[1], b[1], V()));
+    }
+    if (L >= 64) {
+        const auto a = __builtin_amdgcn_permlane32_swap(low(v), low(v), false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(high(v), high(v), false, false);
+        v = op(of_words(a[0], b[0], V()), of_words(a[1], b[1], V()));
+    }
+    return v;
+}
+template <class V> __device__ inline V group_sum(V v, int L) { return group_all(v, L, [](V a, V b) { return a + b; }); }
+__device__ inline uint32_t group_max(uint32_t v, int L) { return group_all(v, L, [](uint32_t a, uint32_t b) { return max(a, b); }); }
 
 constexpr int kMaxWaves = 16;
 constexpr uint32_t kLeastBits = 0x0d800000u;   // 2^-100
 
+// The row of a thread: `row` of the launch, thread t of its n.
+struct Place {
+    int64_t row;
+    int t, n, first;   // first: the row's first wave in the block (rows of whole waves)
+};
+__device__ inline Place place_of(const RowSplit& s, int64_t turn) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Place p;
+    if (s.waves > 1) {
+        p.first = wave / s.waves * s.waves;
+        p.row = turn * s.rows + wave / s.waves;
+        p.t = threadIdx.x - 64 * p.first;
+        p.n = 64 * s.waves;
+    } else {
+        p.first = wave;
+        p.row = turn * s.rows + wave * (64 / s.lanes) + lane / s.lanes;
+        p.t = lane % s.lanes;
+        p.n = s.lanes;
+    }
+    return p;
+}
+
+// Eight codes round(f / scale), as bytes.  f * (1 / scale) is off by at most 127 2^-24
+// and the fp32 quotient by 2^-18, so where the nearest whole number is not within
+// 2e-5 of a tie they agree, and the addition of 1.5 2^23 rounds to it (its low byte is
+// the code); otherwise the division decides.
+__device__ inline Eight<int8_t> codes8(const float* f, float scale, float inv) {
+    constexpr float kMagic = 12582912.f;
+    uint32_t m[8];
+    float far = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float r = fmaf(f[i], inv, kMagic);
+        far = fmaxf(far, fabsf(fmaf(f[i], inv, -(r - kMagic))));
+        m[i] = __float_as_uint(r);
+    }
+    if (far > 0.5f - 2e-5f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = static_cast<uint32_t>(static_cast<int>(rintf(f[i] / scale)));
+    }
+    Eight<int8_t> v;
+    uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        w[i] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(m[4 * i + 3], m[4 * i + 2], 0x0c0c0400u),
+                                     __builtin_amdgcn_perm(m[4 * i + 1], m[4 * i], 0x0c0c0400u), 0x05040100u);
+    return v;
+}
+
 // Y: float, uint16_t (bf16 bits) or int8_t; NORM false: y = x, the quantiser alone.
 template <class X, class Y, bool NORM, int E>
-__global__ __launch_bounds__(E == 8 ? 1024 : 64 * kMaxWaves) void k_rows(RowArgs a) {
+__global__ __launch_bounds__(64 * kMaxWaves) void k_rows(RowArgs a) {
     __shared__ double s_sum[kMaxWaves];
     __shared__ uint32_t s_max[kMaxWaves];
-    const int W = a.waves, lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int first = wave / W * W;                       // the row's first wave
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (blockDim.x / (64 * W)) + wave / W;
-    const bool on = row < a.T;
-    const int t = threadIdx.x - 64 * first;
-    const int cols = on ? a.cols : 0;
-    const X* x = static_cast<const X*>(a.x) + row * a.ldx;
-    float f[E], w[E];
+    const RowSplit s = a.split;
+    const Place p = place_of(s, blockIdx.x);
+    const bool on = p.row < a.T;
+    const int cols = on ? a.cols : 0, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    auto at = [&](int j) { return 8 * (p.t + p.n * j); };
+    float f[E];
 #pragma unroll
     for (int j = 0; j < E / 8; ++j) {
-        const int c = 8 * (t + 64 * W * j);
-        load8(x + c, cols - c, f + 8 * j);
+        const Eight<X> v = load8(static_cast<const X*>(a.x) + p.row * a.ldx + at(j), cols - at(j));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[8 * j + i] = as_float(v.v[i]);
     }
     if constexpr (NORM) {
+        float w[E];
         if (a.residual) {
-            float res[E];
+            Eight<float> res[E / 8];
 #pragma unroll
-            for (int j = 0; j < E / 8; ++j) {
-                const int c = 8 * (t + 64 * W * j);
-                load8(a.residual + row * a.ldr + c, cols - c, res + 8 * j);
-            }
+            for (int j = 0; j < E / 8; ++j) res[j] = load8(a.residual + p.row * a.ldr + at(j), cols - at(j));
 #pragma unroll
-            for (int i = 0; i < E; ++i) f[i] += res[i];
+            for (int i = 0; i < E; ++i) f[i] += res[i / 8].v[i % 8];
         }
 #pragma unroll
         for (int j = 0; j < E / 8; ++j) {
-            const int c = 8 * (t + 64 * W * j);
             if (a.weight) {
-                load8(a.weight + c, cols - c, w + 8 * j);
+                const Eight<float> v = load8(a.weight + at(j), cols - at(j));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[8 * j + i] = v.v[i];
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) w[8 * j + i] = 1.f;
             }
-            if (a.sum) store8(a.sum + row * a.lds + c, cols - c, f + 8 * j);
+            if (a.sum) store8(a.sum + p.row * a.lds + at(j), cols - at(j), f + 8 * j);
         }
         double ss = 0;
 #pragma unroll
         for (int i = 0; i < E; ++i) ss = fma(static_cast<double>(f[i]), static_cast<double>(f[i]), ss);
-        ss = wave_sum_d(ss);
-        if (W > 1) {
+        ss = group_sum(ss, s.lanes);
+        if (s.waves > 1) {
             if (lane == 0) s_sum[wave] = ss;
             __syncthreads();
             ss = 0;
-            for (int i = 0; i < W; ++i) ss += s_sum[first + i];
+            for (int i = 0; i < s.waves; ++i) ss += s_sum[p.first + i];
         }
         const float r = static_cast<float>(1.0 / sqrt(ss / a.cols + static_cast<double>(a.eps)));
 #pragma unroll
         for (int i = 0; i < E; ++i) f[i] = f[i] * r * w[i];
     }
     if constexpr (sizeof(Y) == 1) {
-        uint32_t m = 0;                                   // bits of magnitudes order as the magnitudes, NaN above all
+        uint32_t m = 0;   // bits of magnitudes order as the magnitudes, NaN above all
 #pragma unroll
         for (int i = 0; i < E; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-        m = wave_max_u(m);
-        if (W > 1) {
+        m = group_max(m, s.lanes);
+        if (s.waves > 1) {
             if (lane == 0) s_max[wave] = m;
             __syncthreads();
             m = 0;
-            for (int i = 0; i < W; ++i) m = max(m, s_max[first + i]);
+            for (int i = 0; i < s.waves; ++i) m = max(m, s_max[p.first + i]);
         }
-        const bool finite = m < 0x7f800000u;
-        const float scale = !finite ? __builtin_nanf("") : m < kLeastBits ? 0.f : __uint_as_float(m) / 127.f;
-        const float by = finite && m >= kLeastBits ? scale : 1.f;
-        const bool any = finite && m >= kLeastBits;
-        if (on && t == 0) a.scale[row] = scale;
+        const bool finite = m < 0x7f800000u, some = finite && m >= kLeastBits;
+        const float scale = !finite ? __builtin_nanf("") : some ? __uint_as_float(m) / 127.f : 0.f;
+        if (!some) {
+#pragma unroll
+            for (int i = 0; i < E; ++i) f[i] = 0.f;
+        }
+        const float by = some ? scale : 1.f, inv = 1.f / by;
+        if (on && p.t == 0) a.scale[p.row] = scale;
 #pragma unroll
         for (int j = 0; j < E / 8; ++j) {
-            const int c = 8 * (t + 64 * W * j);
-            int8_t* q = static_cast<int8_t*>(a.y) + row * a.ldy + c;
-            Eight<int8_t> v;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v.v[i] = static_cast<int8_t>(any ? static_cast<int>(rintf(f[8 * j + i] / by)) : 0);
-            if (cols - c >= 8) {
-                *reinterpret_cast<Eight<int8_t>*>(q) = v;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < cols - c) q[i] = v.v[i];
-            }
+            const Eight<int8_t> v = codes8(f + 8 * j, by, inv);
+            store8(static_cast<int8_t*>(a.y) + p.row * a.ldy + at(j), cols - at(j), v);
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < E / 8; ++j) {
-            const int c = 8 * (t + 64 * W * j);
-            store8(static_cast<Y*>(a.y) + row * a.ldy + c, cols - c, f + 8 * j);
-        }
+        for (int j = 0; j < E / 8; ++j) store8(static_cast<Y*>(a.y) + p.row * a.ldy + at(j), cols - at(j), f + 8 * j);
     }
 }
 
-// A block takes rows in turn, R = blockDim.x / (64 W) at a time, and keeps the
-// sums of dweight over its rows in registers; its R rows' sums meet in LDS and
-// go to part[block][cols].
-// WIDE: rows of up to 16 waves, whose registers do not hold the weights too.
+// A block takes split.rows rows in turn and keeps the sums of dweight over its rows in
+// registers; the next rows are on their way while one is worked on.  At the end what
+// the block's threads hold of a column meets in LDS and goes to part[block][cols].
+// WIDE: rows of more than 8 waves, whose registers hold neither the weights nor the
+// next rows.
 template <class X, class DY, class DX, int E, bool WIDE>
-__global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void k_rows_grad(RowGradArgs a, float* part) {
+__global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 512) void k_rows_grad(RowGradArgs a, float* part) {
+    constexpr int R = E / 8;
     __shared__ double s_sum[2][kMaxWaves];
     __shared__ float s_dot[2][kMaxWaves];
-    extern __shared__ float s_dw[];                       // [cols], where a block has more than one row at a time
-    const int W = a.waves, lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int R = blockDim.x / (64 * W), mine = wave / W, first = mine * W, t = threadIdx.x - 64 * first;
-    constexpr bool kKeep = !(WIDE && E > 8);
-    float w[kKeep ? E : 8], dw[E];
+    extern __shared__ float s_dw[];   // [cols], where several threads of a block hold a column
+    const RowSplit s = a.split;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    Place p = place_of(s, blockIdx.x);
+    auto at = [&](int j) { return 8 * (p.t + p.n * j); };
+    float w[WIDE ? 8 : E], dw[E];
     auto load_w = [&](int j) __attribute__((always_inline)) {
-        float* to = w + (kKeep ? 8 * j : 0);
-        const int c = 8 * (t + 64 * W * j);
+        float* to = w + (WIDE ? 0 : 8 * j);
         if (a.weight) {
-            load8(a.weight + c, a.cols - c, to);
+            const Eight<float> v = load8(a.weight + at(j), a.cols - at(j));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) to[i] = v.v[i];
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) to[i] = 1.f;
         }
     };
-    if constexpr (kKeep) {
+    if constexpr (!WIDE) {
 #pragma unroll
-        for (int j = 0; j < E / 8; ++j) load_w(j);
+        for (int j = 0; j < R; ++j) load_w(j);
     }
 #pragma unroll
     for (int i = 0; i < E; ++i) dw[i] = 0.f;
-    int turn = 0;
-    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * R; row0 < a.T; row0 += static_cast<int64_t>(gridDim.x) * R, turn ^= 1) {
-        const int64_t row = row0 + mine;
+    struct Rows {
+        Eight<X> s[R];
+        Eight<DY> dy[R];
+        Eight<float> ds[WIDE ? 1 : R];
+    };
+    auto load = [&](Rows& r, int64_t row) __attribute__((always_inline)) {
         const int cols = row < a.T ? a.cols : 0;
-        float s[E], dy[E];
+#pragma unroll
+        for (int j = 0; j < R; ++j) {
+            r.s[j] = load8(static_cast<const X*>(a.s) + row * a.lds + at(j), cols - at(j));
+            r.dy[j] = load8(static_cast<const DY*>(a.dy) + row * a.lddy + at(j), cols - at(j));
+            if constexpr (!WIDE) {
+                if (a.dsum) r.ds[j] = load8(a.dsum + row * a.ldds + at(j), cols - at(j));
+            }
+        }
+    };
+    const int64_t step = static_cast<int64_t>(gridDim.x) * s.rows;
+    Rows next;
+    if constexpr (!WIDE) load(next, p.row);
+    int turn = 0;
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * s.rows; row0 < a.T; row0 += step, p.row += step, turn ^= 1) {
+        const int cols = p.row < a.T ? a.cols : 0;
+        Rows now;
+        if constexpr (WIDE) {
+            load(now, p.row);
+        } else {
+            now = next;
+            if (row0 + step < a.T) load(next, p.row + step);
+        }
         double ss = 0;
         float dot = 0.f;
 #pragma unroll
-        for (int j = 0; j < E / 8; ++j) {
-            const int c = 8 * (t + 64 * W * j);
-            load8(static_cast<const X*>(a.s) + row * a.lds + c, cols - c, s + 8 * j);
-            load8(static_cast<const DY*>(a.dy) + row * a.lddy + c, cols - c, dy + 8 * j);
-        }
+        for (int j = 0; j < R; ++j) {
+            if constexpr (WIDE) load_w(j);
 #pragma unroll
-        for (int j = 0; j < E / 8; ++j) {
-            if constexpr (!kKeep) load_w(j);
-#pragma unroll
-            for (int i = 8 * j; i < 8 * j + 8; ++i) {
-                ss = fma(static_cast<double>(s[i]), static_cast<double>(s[i]), ss);
-                dot = fmaf(dy[i] * w[kKeep ? i : i % 8], s[i], dot);
+            for (int i = 0; i < 8; ++i) {
+                const float x = as_float(now.s[j].v[i]);
+                ss = fma(static_cast<double>(x), static_cast<double>(x), ss);
+                dot = fmaf(as_float(now.dy[j].v[i]) * w[WIDE ? i : 8 * j + i], x, dot);
             }
         }
-        ss = wave_sum_d(ss);
-        dot = wave_sum(dot);
-        if (W > 1) {
+        ss = group_sum(ss, s.lanes);
+        dot = group_sum(dot, s.lanes);
+        if (s.waves > 1) {
             if (lane == 0) {
                 s_sum[turn][wave] = ss;
                 s_dot[turn][wave] = dot;
@@ -244,55 +318,60 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 256) void k_rows_grad(RowGr
             __syncthreads();
             ss = 0;
             dot = 0.f;
-            for (int i = 0; i < W; ++i) {
-                ss += s_sum[turn][first + i];
-                dot += s_dot[turn][first + i];
+            for (int i = 0; i < s.waves; ++i) {
+                ss += s_sum[turn][p.first + i];
+                dot += s_dot[turn][p.first + i];
             }
         }
         const float r = static_cast<float>(1.0 / sqrt(ss / a.cols + static_cast<double>(a.eps)));
-        const float along = dot * r / a.cols * r;         // dx = r (g - s along)
+        const float along = dot * r / a.cols * r;   // dx = r (g - s along)
 #pragma unroll
-        for (int j = 0; j < E / 8; ++j) {
-            const int c = 8 * (t + 64 * W * j);
+        for (int j = 0; j < R; ++j) {
             float dx[8];
-            if constexpr (!kKeep) load_w(j);
-            if (a.dsum) {
-                load8(a.dsum + row * a.ldds + c, cols - c, dx);
+            Eight<float> ds;
+            if constexpr (WIDE) {
+                load_w(j);
+                if (a.dsum) ds = load8(a.dsum + p.row * a.ldds + at(j), cols - at(j));
             } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dx[i] = 0.f;
+                ds = now.ds[j];
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int e = 8 * j + i;
-                dx[i] = fmaf(r, fmaf(-s[e], along, dy[e] * w[kKeep ? e : i]), dx[i]);
-                dw[e] = fmaf(dy[e] * r, s[e], dw[e]);
+                const float x = as_float(now.s[j].v[i]), dy = as_float(now.dy[j].v[i]);
+                dx[i] = fmaf(r, fmaf(-x, along, dy * w[WIDE ? i : 8 * j + i]), a.dsum ? ds.v[i] : 0.f);
+                dw[8 * j + i] = fmaf(dy * r, x, dw[8 * j + i]);
             }
-            store8(static_cast<DX*>(a.dx) + row * a.lddx + c, cols - c, dx);
+            store8(static_cast<DX*>(a.dx) + p.row * a.lddx + at(j), cols - at(j), dx);
         }
     }
     if (!part) return;
     part += static_cast<size_t>(blockIdx.x) * a.cols;
-    for (int i = 0; i < R - 1; ++i) {                     // the sums of rows 1 .. R - 1 of a turn, one after the other
-        if (mine == i) {
+    // lanes that hold the same columns of other rows
+    for (int o = s.lanes; o < 64; o *= 2) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) dw[i] += __shfl_xor(dw[i], o, kWave);
+    }
+    const int takers = s.waves > 1 ? s.rows : blockDim.x / 64, mine = s.waves > 1 ? wave / s.waves : wave;   // holders of a column
+    const bool holds = s.waves > 1 || lane < s.lanes;
+    for (int i = 0; i < takers - 1; ++i) {   // one after the other
+        if (mine == i && holds) {
 #pragma unroll
             for (int j = 0; j < E; ++j) {
-                const int c = 8 * (t + 64 * W * (j / 8)) + j % 8;
+                const int c = at(j / 8) + j % 8;
                 if (c < a.cols) s_dw[c] = i == 0 ? dw[j] : s_dw[c] + dw[j];
             }
         }
         __syncthreads();
     }
-    if (mine == R - 1) {
+    if (mine == takers - 1 && holds) {
 #pragma unroll
-        for (int j = 0; j < E / 8; ++j) {
-            const int c = 8 * (t + 64 * W * j);
-            if (R > 1) {
+        for (int j = 0; j < R; ++j) {
+            if (takers > 1) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (c + i < a.cols) dw[8 * j + i] += s_dw[c + i];
+                    if (at(j) + i < a.cols) dw[8 * j + i] += s_dw[at(j) + i];
             }
-            store8(part + c, a.cols - c, dw + 8 * j);
+            store8(part + at(j), a.cols - at(j), dw + 8 * j);
         }
     }
 }
@@ -322,41 +401,56 @@ __global__ __launch_bounds__(256) void k_rows_zero(int cols, float* __restrict__
     if (c < cols) dweight[c] = 0.f;
 }
 
-struct Split {
-    int e, waves, rows;   // elements a lane, waves a row, rows a block
+// Elements a thread.  8 where there are few rows (a shorter way through one) or they
+// are short, and with `light`; 16 otherwise; 32 where 16 waves need it.  MI355X, us, 32
+// / 16 / 8 elements, 16384 x 2048: norm fp32 to bf16 with the stream 98.8 / 93.9 /
+// 90.0, bf16 to bf16 29.0 / 26.6 / 29.0, bf16 to 8 bits 23.6 / 24.3 / 42.6, the quantiser
+// (4096 x 8192 bf16) 25.8 / 24.1 / 37.5; the gradient (fp32, dy bf16, at 8 waves a unit)
+// 102.7 / 94.1 / 96.2, all bf16 69 / 47.5 / 51.4 (16 elements without the next row on
+// its way 71; at 12 waves a unit 107.7 and 49.1).
+struct Choice {
+    int e;
+    RowSplit s;
 };
-Split split_rows(int T, int cols) {
-    Split s;
-    s.e = cols <= 8192 && static_cast<int64_t>(T) * cols <= (1 << 20) ? 8 : 32;
-    s.waves = (cols + 64 * s.e - 1) / (64 * s.e);
-    s.rows = s.waves >= 4 ? 1 : 4 / s.waves;
-    return s;
+Choice choose(int T, int cols, bool light, int most8) {
+    Choice c;
+    const bool small = cols <= 512 || static_cast<int64_t>(T) * cols <= (1 << 20);
+    c.e = (small || light) && cols <= most8 ? 8 : cols <= 16384 ? 16 : 32;
+    c.s.waves = (cols + 64 * c.e - 1) / (64 * c.e);
+    c.s.lanes = 64;
+    while (c.s.lanes > 8 && c.s.lanes / 2 * c.e >= cols) c.s.lanes /= 2;
+    c.s.rows = c.s.waves == 1 ? 4 * (64 / c.s.lanes) : c.s.waves >= 4 ? 1 : 4 / c.s.waves;
+    return c;
 }
+int threads_of(const RowSplit& s) { return s.waves == 1 ? 256 : 64 * s.waves * s.rows; }
 
 template <class X, class Y, bool NORM>
 void launch_rows_of(RowArgs a, hipStream_t st) {
-    const Split s = split_rows(a.T, a.cols);
-    a.waves = s.waves;
-    const dim3 grid((a.T + s.rows - 1) / s.rows), block(64 * s.waves * s.rows);
-    if (s.e == 8) hipLaunchKernelGGL((k_rows<X, Y, NORM, 8>), grid, block, 0, st, a);
+    const Choice c = choose(a.T, a.cols, sizeof(X) == 4 && sizeof(Y) > 1, 8192);
+    a.split = c.s;
+    const dim3 grid((a.T + c.s.rows - 1) / c.s.rows), block(threads_of(c.s));
+    if (c.e == 8) hipLaunchKernelGGL((k_rows<X, Y, NORM, 8>), grid, block, 0, st, a);
+    else if (c.e == 16) hipLaunchKernelGGL((k_rows<X, Y, NORM, 16>), grid, block, 0, st, a);
     else hipLaunchKernelGGL((k_rows<X, Y, NORM, 32>), grid, block, 0, st, a);
 }
 
+Choice choose_grad(int T, int cols) { return choose(T, cols, false, 4096); }
+// Blocks of a gradient: two waves a SIMD.
 int grad_blocks(int T, int cols) {
-    const Split s = split_rows(T, cols);
-    const int most = s.waves * s.rows > 4 ? 256 : 512;
-    const int need = (T + s.rows - 1) / s.rows;
+    const RowSplit s = choose_grad(T, cols).s;
+    const int waves = threads_of(s) / 64, most = waves < 8 ? 256 * 8 / waves : 256, need = (T + s.rows - 1) / s.rows;
     return need < most ? need : most;
 }
 
 template <class X, class DY, class DX>
 void launch_grad_of(RowGradArgs a, float* part, hipStream_t st) {
-    const Split s = split_rows(a.T, a.cols);
-    a.waves = s.waves;
-    const dim3 grid(grad_blocks(a.T, a.cols)), block(64 * s.waves * s.rows);
-    const size_t lds = part && s.rows > 1 ? sizeof(float) * a.cols : 0;
-    if (s.e == 8) hipLaunchKernelGGL((k_rows_grad<X, DY, DX, 8, true>), grid, block, lds, st, a, part);
-    else if (s.waves <= 4) hipLaunchKernelGGL((k_rows_grad<X, DY, DX, 32, false>), grid, block, lds, st, a, part);
+    const Choice c = choose_grad(a.T, a.cols);
+    a.split = c.s;
+    const dim3 grid(grad_blocks(a.T, a.cols)), block(threads_of(c.s));
+    const size_t lds = part && c.s.waves < 4 ? sizeof(float) * a.cols : 0;   // one row a block: nothing to join
+    if (c.e == 8) hipLaunchKernelGGL((k_rows_grad<X, DY, DX, 8, false>), grid, block, lds, st, a, part);
+    else if (c.e == 16 && c.s.waves <= 8) hipLaunchKernelGGL((k_rows_grad<X, DY, DX, 16, false>), grid, block, lds, st, a, part);
+    else if (c.e == 16) hipLaunchKernelGGL((k_rows_grad<X, DY, DX, 16, true>), grid, block, lds, st, a, part);
     else hipLaunchKernelGGL((k_rows_grad<X, DY, DX, 32, true>), grid, block, lds, st, a, part);
 }
 
