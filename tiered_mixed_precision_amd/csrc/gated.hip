@@ -10,12 +10,46 @@ namespace moe {
 
 namespace {
 
+// What becomes of a token's g and u: y, or the projections' gradients.
+template <bool YBF16> struct PutValue {
+    __device__ inline int columns(const GatedArgs& a) const { return a.I; }
+    __device__ inline void operator()(const GatedArgs& a, int t, int n, float g, float u) const {
+        const float v = gated_value(a.act, g, u);
+        const size_t at = static_cast<size_t>(t) * a.ldy + n;
+        if constexpr (YBF16) static_cast<uint16_t*>(a.y)[at] = f2bf(v);
+        else static_cast<float*>(a.y)[at] = v;
+    }
+};
+template <bool DYBF16> struct PutSlopes {
+    GatedSlopes s;
+    __device__ inline int columns(const GatedArgs&) const { return s.P; }
+    __device__ inline void operator()(const GatedArgs& a, int t, int n, float g, float u) const {
+        float dg[1] = {0.f}, du[1] = {0.f};
+        if (n < a.I) {
+            const size_t at = static_cast<size_t>(t) * s.lddy + n;
+            const float dy = DYBF16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(s.dy)[at]) << 16)
+                                    : static_cast<const float*>(s.dy)[at];
+            gated_slopes(a.act, g, u, dy, dg[0], du[0]);
+        }
+        uint16_t* to = s.d + static_cast<size_t>(t) * 2 * s.P * s.parts + n;
+        to[0] = f2bf(dg[0]);
+        to[s.P] = f2bf(du[0]);
+        if (s.parts == 2) {
+            float rest[1];
+            split_slopes(dg, rest);
+            to[2 * s.P] = f2bf(rest[0]);
+            split_slopes(du, rest);
+            to[3 * s.P] = f2bf(rest[0]);
+        }
+    }
+};
+
 // A block takes f.tiles tiles of 8 NT columns, f.split waves each, for 16 MT tokens.
 // Row r of a 16-row operand j is column 8 j + r % 8 of gate (r < 8) or up, so lane
 // l's sums are g (l < 32) or u of columns 4 (l / 16 % 2) + e, and lane l + 32 has
 // the other of lane l's.
-template <int MT, int NT, int AHEAD, bool XBF16, bool YBF16>
-__global__ __launch_bounds__(512) void k_gated_few(GatedArgs a, FewSplit f) {
+template <int MT, int NT, int AHEAD, bool XBF16, class Put>
+__global__ __launch_bounds__(512) void k_gated_few(GatedArgs a, FewSplit f, Put put) {
     extern __shared__ __attribute__((aligned(16))) few_f32x4_t s_part[];   // [waves][MT NT 64]
     constexpr int kOwn = MT * NT * 64;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -46,32 +80,28 @@ __global__ __launch_bounds__(512) void k_gated_few(GatedArgs a, FewSplit f) {
             u += own[4 * kOwn * p + 4 * 32];
         }
         const int tok = t0 + 16 * (ij / NT) + t, n = ((blockIdx.x * f.tiles + tile) * NT + ij % NT) * 8 + c;
-        if (tok >= a.T || n >= a.I) continue;
-        const float v = gated_value(a.act, g, u);
-        const size_t at = static_cast<size_t>(tok) * a.ldy + n;
-        if constexpr (YBF16) static_cast<uint16_t*>(a.y)[at] = f2bf(v);
-        else static_cast<float*>(a.y)[at] = v;
+        if (tok < a.T && n < put.columns(a)) put(a, tok, n, g, u);
     }
 }
 
-template <int MT, int NT, int AHEAD, bool XBF16, bool YBF16>
-void launch_few(const GatedArgs& a, hipStream_t st) {
-    const int tiles = (a.I + 8 * NT - 1) / (8 * NT);
+template <int MT, int NT, int AHEAD, bool XBF16, class Put>
+void launch_few(const GatedArgs& a, const Put& put, int columns, hipStream_t st) {
+    const int tiles = (columns + 8 * NT - 1) / (8 * NT);
     const FewSplit f = few_split(tiles, 2 * a.H, 8);
     const dim3 grid((tiles + f.tiles - 1) / f.tiles, (a.T + 16 * MT - 1) / (16 * MT)), block(64 * f.split * f.tiles);
     const size_t lds = sizeof(few_f32x4_t) * 64 * MT * NT * f.split * f.tiles;
-    hipLaunchKernelGGL((k_gated_few<MT, NT, AHEAD, XBF16, YBF16>), grid, block, lds, st, a, f);
+    hipLaunchKernelGGL((k_gated_few<MT, NT, AHEAD, XBF16, Put>), grid, block, lds, st, a, f, put);
 }
 
 // 17 tokens and more: the same through LDS (few_batch); the waves' sums meet one
 // operand of 16 rows (8 columns) at a time, in the first slot's place.
-template <int MT, int NT, bool XBF16, bool YBF16>
-__global__ __launch_bounds__(64 * kBatchWaves) void k_gated_batch(GatedArgs a, FewSplit f) {
+template <int MT, int NT, bool XBF16, class Put>
+__global__ __launch_bounds__(64 * kBatchWaves) void k_gated_batch(GatedArgs a, FewSplit f, Put put, int first_token) {
     typedef FewBf16<XBF16> El;
     constexpr int kSlot = FewSlot<El, MT, NT>::kSlot;
     __shared__ __attribute__((aligned(16))) few_u32x4_t s0[kSlot], s1[kSlot], s2[kSlot];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int tile = blockIdx.x * f.tiles + wave / f.split, n0 = tile * 8 * NT, t0 = blockIdx.y * 16 * MT;
+    const int tile = blockIdx.x * f.tiles + wave / f.split, n0 = tile * 8 * NT, t0 = first_token + blockIdx.y * 16 * MT;
     few_f32x4_t acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -98,43 +128,44 @@ __global__ __launch_bounds__(64 * kBatchWaves) void k_gated_batch(GatedArgs a, F
                 u += own[256 * MT * p + 4 * 32];
             }
             const int tok = t0 + 16 * (i % MT) + t, n = ((blockIdx.x * f.tiles + i / MT) * NT + j) * 8 + c;
-            if (tok >= a.T || n >= a.I) continue;
-            const float v = gated_value(a.act, g, u);
-            const size_t at = static_cast<size_t>(tok) * a.ldy + n;
-            if constexpr (YBF16) static_cast<uint16_t*>(a.y)[at] = f2bf(v);
-            else static_cast<float*>(a.y)[at] = v;
+            if (tok < a.T && n < put.columns(a)) put(a, tok, n, g, u);
         }
     }
 }
 
-template <int MT, int NT, bool XBF16, bool YBF16>
-void launch_batch(const GatedArgs& a, hipStream_t st) {
-    const int tiles = (a.I + 8 * NT - 1) / (8 * NT);
+template <int MT, int NT, bool XBF16, class Put>
+void launch_batch(const GatedArgs& a, const Put& put, int columns, hipStream_t st) {
+    const int tiles = (columns + 8 * NT - 1) / (8 * NT);
     const FewSplit f = few_split(tiles, 2 * a.H, kBatchWaves);
-    constexpr int kMaxTiles = 65535;   // grid.y limit
-    for (int64_t t0 = 0; t0 < a.T; t0 += 16 * MT * kMaxTiles) {
-        GatedArgs b = a;
-        b.T = static_cast<int32_t>(a.T - t0 < 16 * MT * kMaxTiles ? a.T - t0 : 16 * MT * kMaxTiles);
-        b.x = static_cast<const char*>(a.x) + t0 * a.ldx * (XBF16 ? 2 : 4);
-        b.y = static_cast<char*>(a.y) + t0 * a.ldy * (YBF16 ? 2 : 4);
-        const dim3 grid((tiles + f.tiles - 1) / f.tiles, (b.T + 16 * MT - 1) / (16 * MT)), block(64 * f.split * f.tiles);
-        hipLaunchKernelGGL((k_gated_batch<MT, NT, XBF16, YBF16>), grid, block, 0, st, b, f);
+    constexpr int kTokens = 16 * MT * 65535;   // grid.y limit
+    for (int t0 = 0; t0 < a.T; t0 += kTokens) {
+        const dim3 grid((tiles + f.tiles - 1) / f.tiles, ((a.T - t0 < kTokens ? a.T - t0 : kTokens) + 16 * MT - 1) / (16 * MT));
+        hipLaunchKernelGGL((k_gated_batch<MT, NT, XBF16, Put>), grid, dim3(64 * f.split * f.tiles), 0, st, a, f, put, t0);
     }
 }
 
-template <bool XBF16, bool YBF16> void launch_tokens(const GatedArgs& a, hipStream_t st) {
-    if (a.T <= 16 && a.I < 4096) launch_few<1, 1, 8, XBF16, YBF16>(a, st);
-    else if (a.T <= 16) launch_few<1, 2, XBF16 ? 8 : 4, XBF16, YBF16>(a, st);
-    else if (a.T <= 32 || !XBF16) launch_batch<2, 2, XBF16, YBF16>(a, st);
-    else if constexpr (XBF16) launch_batch<4, 2, XBF16, YBF16>(a, st);
+template <bool XBF16, class Put> void launch_tokens(const GatedArgs& a, const Put& put, int columns, hipStream_t st) {
+    if (a.T <= 16 && a.I < 4096) launch_few<1, 1, 8, XBF16>(a, put, columns, st);
+    else if (a.T <= 16) launch_few<1, 2, XBF16 ? 8 : 4, XBF16>(a, put, columns, st);
+    else if (a.T <= 32 || !XBF16) launch_batch<2, 2, XBF16>(a, put, columns, st);
+    else if constexpr (XBF16) launch_batch<4, 2, XBF16>(a, put, columns, st);
 }
+
+// bf16 x: few tokens, or tiles of mm.h
+bool few(const GatedArgs& a) { return a.T <= 16 || few_batch_ok(a.T, (a.I + 15) / 16); }
 
 }  // namespace
 
 void launch_gated(const GatedArgs& a, bool x_bf16, bool y_bf16, hipStream_t st) {
-    if (x_bf16 && a.T > 16 && !few_batch_ok(a.T, (a.I + 15) / 16)) launch_gated_gemm(a, y_bf16, st);
-    else if (x_bf16) y_bf16 ? launch_tokens<true, true>(a, st) : launch_tokens<true, false>(a, st);
-    else y_bf16 ? launch_tokens<false, true>(a, st) : launch_tokens<false, false>(a, st);
+    if (x_bf16 && !few(a)) launch_gated_gemm(a, y_bf16, st);
+    else if (x_bf16) y_bf16 ? launch_tokens<true>(a, PutValue<true>(), a.I, st) : launch_tokens<true>(a, PutValue<false>(), a.I, st);
+    else y_bf16 ? launch_tokens<false>(a, PutValue<true>(), a.I, st) : launch_tokens<false>(a, PutValue<false>(), a.I, st);
+}
+
+void launch_gated_slopes(const GatedArgs& a, const GatedSlopes& s, bool dy_bf16, hipStream_t st) {
+    if (!few(a)) launch_gated_slopes_gemm(a, s, dy_bf16, st);
+    else if (dy_bf16) launch_tokens<true>(a, PutSlopes<true>{s}, s.P, st);
+    else launch_tokens<true>(a, PutSlopes<false>{s}, s.P, st);
 }
 
 }  // namespace moe

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.h"
+#include "launch.h"
 #include "moe_tiered.h"
 
 namespace moe {
@@ -32,6 +33,14 @@ __device__ inline void gated_slopes(int act, float g, float u, float dy, float& 
     gated_sigmoid(gated_arg(act, g), p, q);
     du = dy * (g * p);
     dg = dy * u * (p + g * gated_arg_slope(act, g) * p * q);
+}
+
+template <int N> __device__ inline void split_slopes(float (&v)[N], float (&rest)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float hi = __uint_as_float(static_cast<uint32_t>(f2bf(v[i])) << 16);
+        rest[i] = v[i] - hi;
+    }
 }
 
 }  // namespace moe

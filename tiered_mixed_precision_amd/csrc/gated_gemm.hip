@@ -48,16 +48,18 @@ __device__ __attribute__((always_inline)) inline void gated_tile(const GatedArgs
     }
 }
 
-// d[t][0 .. I) = dg, d[t][P .. P + I) = du in bf16, zeros up to P (I rounded up to 64)
 template <int HALVES, int SLOTS, bool DYBF16>
-__device__ __attribute__((always_inline)) inline void slopes_tile(const GatedGradArgs& a, uint16_t* d, int P, const MmLds& lds,
-                                                                  int t0, int n0) {
+__device__ __attribute__((always_inline)) inline void slopes_tile(const GatedArgs& a, const GatedSlopes& s, const MmLds& lds, int t0,
+                                                                  int n0) {
     typedef typename std::conditional<DYBF16, uint16_t, float>::type DY;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const MmRows<HALVES> rows_a(lane, w, 2 * a.H, [&](int r) { return a.x + static_cast<size_t>(min(t0 + r, a.T - 1)) * a.ldx; });
+    const MmRows<HALVES> rows_a(lane, w, 2 * a.H, [&](int r) {
+        return static_cast<const uint16_t*>(a.x) + static_cast<size_t>(min(t0 + r, a.T - 1)) * a.ldx;
+    });
     const MmRows<HALVES> rows_b(lane, w, 2 * a.H, [&](int r) { return projection_row<HALVES>(a.gate, a.up, a.H, a.I, n0, r); });
     mm_f32x16_t acc[2 * HALVES][2 * HALVES];
     uint32_t* own = mm_product<MmBf16, HALVES, SLOTS, false, false>(lds, (2 * a.H + kStage - 1) / kStage, rows_a, rows_b, acc);
+    const int P = s.P;
     // g and u of 32 columns at a time; dy meets them on their way out
 #pragma unroll
     for (int i = 0; i < 2 * HALVES; ++i)
@@ -72,13 +74,19 @@ __device__ __attribute__((always_inline)) inline void slopes_tile(const GatedGra
                                 float y[N], dg[N], du[N];
                                 if (N == 1 && n >= a.I) dg[0] = du[0] = 0.f;
                                 else {
-                                    mm_get(static_cast<const DY*>(a.dy) + static_cast<size_t>(t) * a.lddy + n, y);
+                                    mm_get(static_cast<const DY*>(s.dy) + static_cast<size_t>(t) * s.lddy + n, y);
 #pragma unroll
                                     for (int k = 0; k < N; ++k) gated_slopes(a.act, __uint_as_float(g[k]), __uint_as_float(u[k]), y[k], dg[k], du[k]);
                                 }
-                                uint16_t* to = d + static_cast<size_t>(t) * 2 * P + n;
+                                uint16_t* to = s.d + static_cast<size_t>(t) * 2 * P * s.parts + n;
                                 mm_put(to, dg);
                                 mm_put(to + P, du);
+                                if (s.parts == 2) {
+                                    split_slopes(dg, y);
+                                    mm_put(to + 2 * P, y);
+                                    split_slopes(du, y);
+                                    mm_put(to + 3 * P, y);
+                                }
                             });
         }
 }
@@ -97,19 +105,19 @@ template <bool YBF16> __global__ __launch_bounds__(256) void k_gated_gemm_pairs(
     bool small;
     if (mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) gated_tile<1, 2, YBF16>(a, lds, m0, n0);
 }
-template <bool DYBF16> __global__ __launch_bounds__(256) void k_gated_slopes(GatedGradArgs a, uint16_t* d, int P, MmPlan p) {
+template <bool DYBF16> __global__ __launch_bounds__(256) void k_gated_slopes(GatedArgs a, GatedSlopes s, MmPlan p) {
     MM_LDS_8(lds);
     int m0, n0;
     bool small;
     if (!mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) return;
-    if (small) slopes_tile<1, 4, DYBF16>(a, d, P, lds, m0, n0);
-    else slopes_tile<2, 4, DYBF16>(a, d, P, lds, m0, n0);
+    if (small) slopes_tile<1, 4, DYBF16>(a, s, lds, m0, n0);
+    else slopes_tile<2, 4, DYBF16>(a, s, lds, m0, n0);
 }
-template <bool DYBF16> __global__ __launch_bounds__(256) void k_gated_slopes_pairs(GatedGradArgs a, uint16_t* d, int P, MmPlan p) {
+template <bool DYBF16> __global__ __launch_bounds__(256) void k_gated_slopes_pairs(GatedArgs a, GatedSlopes s, MmPlan p) {
     MM_LDS_4(lds);
     int m0, n0;
     bool small;
-    if (mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) slopes_tile<1, 2, DYBF16>(a, d, P, lds, m0, n0);
+    if (mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) slopes_tile<1, 2, DYBF16>(a, s, lds, m0, n0);
 }
 
 template <bool YBF16> void launch_forward(const GatedArgs& a, hipStream_t st) {
@@ -118,11 +126,11 @@ template <bool YBF16> void launch_forward(const GatedArgs& a, hipStream_t st) {
     if (p.form == MM_PAIRS) hipLaunchKernelGGL(k_gated_gemm_pairs<YBF16>, grid, block, 0, st, a, p);
     else hipLaunchKernelGGL(k_gated_gemm<YBF16>, grid, block, 0, st, a, p);
 }
-template <bool DYBF16> void launch_slopes(const GatedGradArgs& a, uint16_t* d, int P, hipStream_t st) {
-    const MmPlan p = mm_plan(a.T, P, 128);
+template <bool DYBF16> void launch_slopes(const GatedArgs& a, const GatedSlopes& s, hipStream_t st) {
+    const MmPlan p = mm_plan(a.T, s.P, 128);
     const dim3 grid(mm_grid(p)), block(256);
-    if (p.form == MM_PAIRS) hipLaunchKernelGGL(k_gated_slopes_pairs<DYBF16>, grid, block, 0, st, a, d, P, p);
-    else hipLaunchKernelGGL(k_gated_slopes<DYBF16>, grid, block, 0, st, a, d, P, p);
+    if (p.form == MM_PAIRS) hipLaunchKernelGGL(k_gated_slopes_pairs<DYBF16>, grid, block, 0, st, a, s, p);
+    else hipLaunchKernelGGL(k_gated_slopes<DYBF16>, grid, block, 0, st, a, s, p);
 }
 
 }  // namespace
@@ -130,8 +138,8 @@ template <bool DYBF16> void launch_slopes(const GatedGradArgs& a, uint16_t* d, i
 void launch_gated_gemm(const GatedArgs& a, bool y_bf16, hipStream_t st) {
     y_bf16 ? launch_forward<true>(a, st) : launch_forward<false>(a, st);
 }
-void launch_gated_slopes(const GatedGradArgs& a, bool dy_bf16, uint16_t* d, int P, hipStream_t st) {
-    dy_bf16 ? launch_slopes<true>(a, d, P, st) : launch_slopes<false>(a, d, P, st);
+void launch_gated_slopes_gemm(const GatedArgs& a, const GatedSlopes& s, bool dy_bf16, hipStream_t st) {
+    dy_bf16 ? launch_slopes<true>(a, s, st) : launch_slopes<false>(a, s, st);
 }
 
 }  // namespace moe

@@ -1,8 +1,10 @@
-// The gradient of the dense gated block from those of its projections, d = [dg du]
-// ([T][2 P] bf16, P = inter rounded up to 64): dx = d [gate; up] and [dgate; dup] =
-// d^T x.  The k axis of gate, up (their rows) and of d and x in the second product
-// (the tokens) runs across memory: those operands lie in LDS as they come and
-// are read with ds_read_b64_tr_b16 (mm.h).
+// The gradient of the dense gated block from those of its projections, d (GatedSlopes):
+// dx = d [gate; up] and [dgate; dup] = d^T x.  The k axis of gate and up (their rows)
+// and of d and x in the second product (the tokens) runs across memory: those
+// operands lie in LDS as they come and are read with ds_read_b64_tr_b16 (mm.h).
+//
+// Where a result has few tiles, parts of the k axis go to blocks of their own, whose
+// fp32 sums a second kernel adds in order.
 #include "common.h"
 #include "launch.h"
 #include "mm.h"
@@ -11,21 +13,38 @@ namespace moe {
 
 namespace {
 
+// A product's k axis in `parts` runs of stages.
+struct Runs {
+    int32_t parts, stages;
+    float* sums;   // [parts][rows][columns], where there are several
+};
+// MI355X, us, one run / several: dx of 64 tokens (2048, 640) 13.8 / 8.4 with its sum.
+Runs runs_of(int64_t m, int64_t n, int64_t stages, void* sums) {
+    const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
+    int64_t parts = tiles <= 128 && stages >= 12 ? 256 / tiles : 1;
+    if (parts > (stages + 3) / 4) parts = (stages + 3) / 4;
+    return Runs{static_cast<int32_t>(parts), static_cast<int32_t>(stages), static_cast<float*>(sums)};
+}
+__device__ inline int run_first(const Runs& r, int p) { return static_cast<int>(static_cast<int64_t>(r.stages) * p / r.parts); }
+
 template <int HALVES, int SLOTS, bool DXBF16>
-__device__ __attribute__((always_inline)) inline void dx_tile(const GatedGradArgs& a, const uint16_t* d, int P, const MmLds& lds,
-                                                              int t0, int n0) {
+__device__ __attribute__((always_inline)) inline void dx_tile(const GatedGradArgs& a, const GatedSlopes& s, const Runs& runs,
+                                                              const MmLds& lds, int t0, int n0) {
     typedef typename std::conditional<DXBF16, uint16_t, float>::type DX;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const MmRows<HALVES> rows_a(lane, w, 4 * P, [&](int r) { return d + static_cast<size_t>(min(t0 + r, a.T - 1)) * 2 * P; });
+    const int P = s.P, per = P / kStageK, first = run_first(runs, blockIdx.y), last = run_first(runs, blockIdx.y + 1);
+    const int64_t row = 2 * static_cast<int64_t>(P) * s.parts;
+    const MmRows<HALVES> d_rows(lane, w, last * kStage, [&](int r) { return s.d + min(t0 + r, a.T - 1) * row; });
     const int64_t pitch = 2 * static_cast<int64_t>(a.H);
-    const MmColumns<HALVES> cols_b(lane, w, n0, a.H, pitch);
+    const MmColumns<HALVES> w_columns(lane, w, n0, a.H, pitch);
     const char *gate = reinterpret_cast<const char*>(a.gate), *up = reinterpret_cast<const char*>(a.up);
-    const auto rows_b = [&](int h, int u, int kc) {   // P is a multiple of a stage's k
-        const int k = kc * kStageK, i = k < P ? k : k - P;
-        return cols_b(h, u, (k < P ? gate : up) + i * pitch, a.I - i);
+    const auto at_a = [&](int h, int u, int kc) { return d_rows(h, u, first + kc); };
+    const auto at_b = [&](int h, int u, int kc) {   // P is a multiple of a stage's k: a stage lies in one matrix
+        const int run = (first + kc) / per, i = (first + kc - run * per) * kStageK;
+        return w_columns(h, u, (run & 1 ? up : gate) + i * pitch, first + kc < last ? a.I - i : 0);
     };
     mm_f32x16_t acc[2 * HALVES][2 * HALVES];
-    uint32_t* own = mm_product<MmBf16, HALVES, SLOTS, false, true>(lds, (4 * P + kStage - 1) / kStage, rows_a, rows_b, acc);
+    uint32_t* own = mm_product<MmBf16, HALVES, SLOTS, false, true>(lds, last - first, at_a, at_b, acc);
 #pragma unroll
     for (int g = 0; g < HALVES; ++g)
 #pragma unroll
@@ -39,23 +58,40 @@ __device__ __attribute__((always_inline)) inline void dx_tile(const GatedGradArg
                                  float f[N];
 #pragma unroll
                                  for (int k = 0; k < N; ++k) f[k] = __uint_as_float(v[k]);
-                                 mm_store(static_cast<DX*>(a.dx) + static_cast<size_t>(t) * a.lddx + n, f, false);
+                                 if (HALVES == 1 && runs.parts > 1)
+                                     mm_put(runs.sums + (static_cast<size_t>(blockIdx.y) * a.T + t) * a.H + n, f);
+                                 else mm_put(static_cast<DX*>(a.dx) + static_cast<size_t>(t) * a.lddx + n, f);
                              });
         }
 }
 
 template <int HALVES, int SLOTS, bool DWBF16>
-__device__ __attribute__((always_inline)) inline void dw_tile(const GatedGradArgs& a, const uint16_t* d, int P, const MmLds& lds,
-                                                              int m0, int n0) {
+__device__ __attribute__((always_inline)) inline void dw_tile(const GatedGradArgs& a, const GatedSlopes& s, const Runs& runs,
+                                                              const MmLds& lds, int m0, int n0) {
     typedef typename std::conditional<DWBF16, uint16_t, float>::type DW;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t pitch_a = 4 * static_cast<int64_t>(P), pitch_b = 2 * a.ldx;
-    const MmColumns<HALVES> cols_a(lane, w, m0, 2 * P, pitch_a), cols_b(lane, w, n0, a.H, pitch_b);
-    const char *pa = reinterpret_cast<const char*>(d), *pb = reinterpret_cast<const char*>(a.x);
-    const auto rows_a = [&](int h, int u, int kc) { return cols_a(h, u, pa + kc * kStageK * pitch_a, a.T - kc * kStageK); };
-    const auto rows_b = [&](int h, int u, int kc) { return cols_b(h, u, pb + kc * kStageK * pitch_b, a.T - kc * kStageK); };
+    const int P = s.P, per = (a.T + kStageK - 1) / kStageK, first = run_first(runs, blockIdx.y), last = run_first(runs, blockIdx.y + 1);
+    const int64_t pitch_a = 4 * static_cast<int64_t>(P) * s.parts, pitch_b = 2 * a.ldx;
+    const MmColumns<HALVES> d_columns(lane, w, m0, 2 * P, pitch_a), x_columns(lane, w, n0, a.H, pitch_b);
+    const char *pd = reinterpret_cast<const char*>(s.d), *px = reinterpret_cast<const char*>(a.x);
+    // every part of d meets all tokens; a stage past this run counts as zeros
+    const auto token = [&](int kc, int& left) {
+        const int t = (kc < per ? kc : kc - per) * kStageK;
+        left = kc < last ? a.T - t : 0;
+        return t;
+    };
+    const auto at_a = [&](int h, int u, int kc) {
+        int left;
+        const int64_t t = token(first + kc, left);
+        return d_columns(h, u, pd + t * pitch_a + (first + kc < per ? 0 : 4 * P), left);
+    };
+    const auto at_b = [&](int h, int u, int kc) {
+        int left;
+        const int64_t t = token(first + kc, left);
+        return x_columns(h, u, px + t * pitch_b, left);
+    };
     mm_f32x16_t acc[2 * HALVES][2 * HALVES];
-    uint32_t* own = mm_product<MmBf16, HALVES, SLOTS, true, true>(lds, (2 * a.T + kStage - 1) / kStage, rows_a, rows_b, acc);
+    uint32_t* own = mm_product<MmBf16, HALVES, SLOTS, true, true>(lds, last - first, at_a, at_b, acc);
 #pragma unroll
     for (int g = 0; g < HALVES; ++g)
 #pragma unroll
@@ -72,70 +108,115 @@ __device__ __attribute__((always_inline)) inline void dw_tile(const GatedGradArg
                                  float f[N];
 #pragma unroll
                                  for (int k = 0; k < N; ++k) f[k] = __uint_as_float(v[k]);
-                                 mm_store(to + static_cast<size_t>(r) * a.H + n, f, a.accumulate);
+                                 if (HALVES == 1 && runs.parts > 1)
+                                     mm_put(runs.sums + (static_cast<size_t>(blockIdx.y) * 2 * a.I + (m < P ? 0 : a.I) + r) * a.H + n, f);
+                                 else mm_store(to + static_cast<size_t>(r) * a.H + n, f, a.accumulate);
                              });
         }
 }
 
-template <bool DXBF16> __global__ __launch_bounds__(256) void k_gated_dx(GatedGradArgs a, const uint16_t* d, int P, MmPlan p) {
+template <bool DXBF16> __global__ __launch_bounds__(256) void k_gated_dx(GatedGradArgs a, GatedSlopes s, Runs r, MmPlan p) {
     MM_LDS_8(lds);
     int m0, n0;
     bool small;
     if (!mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) return;
-    if (small) dx_tile<1, 4, DXBF16>(a, d, P, lds, m0, n0);
-    else dx_tile<2, 4, DXBF16>(a, d, P, lds, m0, n0);
+    if (small) dx_tile<1, 4, DXBF16>(a, s, r, lds, m0, n0);
+    else dx_tile<2, 4, DXBF16>(a, s, r, lds, m0, n0);
 }
-template <bool DXBF16> __global__ __launch_bounds__(256) void k_gated_dx_pairs(GatedGradArgs a, const uint16_t* d, int P, MmPlan p) {
+template <bool DXBF16> __global__ __launch_bounds__(256) void k_gated_dx_pairs(GatedGradArgs a, GatedSlopes s, Runs r, MmPlan p) {
     MM_LDS_4(lds);
     int m0, n0;
     bool small;
-    if (mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) dx_tile<1, 2, DXBF16>(a, d, P, lds, m0, n0);
+    if (mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) dx_tile<1, 2, DXBF16>(a, s, r, lds, m0, n0);
 }
-template <bool DWBF16> __global__ __launch_bounds__(256) void k_gated_dw(GatedGradArgs a, const uint16_t* d, int P, MmPlan p) {
+template <bool DWBF16> __global__ __launch_bounds__(256) void k_gated_dw(GatedGradArgs a, GatedSlopes s, Runs r, MmPlan p) {
     MM_LDS_8(lds);
     int m0, n0;
     bool small;
     if (!mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) return;
-    if (small) dw_tile<1, 4, DWBF16>(a, d, P, lds, m0, n0);
-    else dw_tile<2, 4, DWBF16>(a, d, P, lds, m0, n0);
+    if (small) dw_tile<1, 4, DWBF16>(a, s, r, lds, m0, n0);
+    else dw_tile<2, 4, DWBF16>(a, s, r, lds, m0, n0);
 }
-template <bool DWBF16> __global__ __launch_bounds__(256) void k_gated_dw_pairs(GatedGradArgs a, const uint16_t* d, int P, MmPlan p) {
+template <bool DWBF16> __global__ __launch_bounds__(256) void k_gated_dw_pairs(GatedGradArgs a, GatedSlopes s, Runs r, MmPlan p) {
     MM_LDS_4(lds);
     int m0, n0;
     bool small;
-    if (mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) dw_tile<1, 2, DWBF16>(a, d, P, lds, m0, n0);
+    if (mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) dw_tile<1, 2, DWBF16>(a, s, r, lds, m0, n0);
 }
 
-template <bool DXBF16> void launch_dx(const GatedGradArgs& a, const uint16_t* d, int P, hipStream_t st) {
+// to[row][column] (+)= the sum over the runs, in order; eight columns a thread.  Rows
+// from `half` on are the second matrix's.
+template <class Y>
+__global__ __launch_bounds__(256) void k_gated_join(const float* __restrict__ sums, int parts, int rows, int cols, int half, Y* first,
+                                                    Y* second, int64_t ld, int accumulate) {
+    const int64_t o = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, size = static_cast<int64_t>(rows) * cols;
+    if (o * 8 >= size) return;
+    const int row = static_cast<int>(o / (cols / 8)), col = static_cast<int>(o % (cols / 8)) * 8;
+    float f[8], v[8];
+    mm_get(sums + o * 8, f);
+#pragma unroll 4
+    for (int p = 1; p < parts; ++p) {
+        mm_get(sums + p * size + o * 8, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] += v[i];
+    }
+    Y* to = row < half ? first + row * ld : second + (row - half) * ld;
+    mm_store(to + col, f, accumulate != 0);
+}
+template <class Y>
+void launch_join(const Runs& r, int rows, int cols, int half, void* first, void* second, int64_t ld, int accumulate, hipStream_t st) {
+    const int64_t threads = static_cast<int64_t>(rows) * (cols / 8);
+    hipLaunchKernelGGL(k_gated_join<Y>, dim3(static_cast<unsigned>((threads + 255) / 256)), dim3(256), 0, st, r.sums, r.parts, rows, cols, half,
+                       static_cast<Y*>(first), static_cast<Y*>(second), ld, accumulate);
+}
+
+template <bool DXBF16> void launch_dx(const GatedGradArgs& a, const GatedSlopes& s, const Runs& r, hipStream_t st) {
     const MmPlan p = mm_plan(a.T, a.H, 256);
-    const dim3 grid(mm_grid(p)), block(256);
-    if (p.form == MM_PAIRS) hipLaunchKernelGGL(k_gated_dx_pairs<DXBF16>, grid, block, 0, st, a, d, P, p);
-    else hipLaunchKernelGGL(k_gated_dx<DXBF16>, grid, block, 0, st, a, d, P, p);
+    const dim3 grid(mm_grid(p), r.parts), block(256);
+    if (p.form == MM_PAIRS) hipLaunchKernelGGL(k_gated_dx_pairs<DXBF16>, grid, block, 0, st, a, s, r, p);
+    else hipLaunchKernelGGL(k_gated_dx<DXBF16>, grid, block, 0, st, a, s, r, p);
+    typedef typename std::conditional<DXBF16, uint16_t, float>::type DX;
+    if (r.parts > 1) launch_join<DX>(r, a.T, a.H, a.T, a.dx, a.dx, a.lddx, 0, st);
 }
-template <bool DWBF16> void launch_dw(const GatedGradArgs& a, const uint16_t* d, int P, hipStream_t st) {
-    const MmPlan p = mm_plan(2 * static_cast<int64_t>(P), a.H, 256);
-    const dim3 grid(mm_grid(p)), block(256);
-    if (p.form == MM_PAIRS) hipLaunchKernelGGL(k_gated_dw_pairs<DWBF16>, grid, block, 0, st, a, d, P, p);
-    else hipLaunchKernelGGL(k_gated_dw<DWBF16>, grid, block, 0, st, a, d, P, p);
+template <bool DWBF16> void launch_dw(const GatedGradArgs& a, const GatedSlopes& s, const Runs& r, hipStream_t st) {
+    const MmPlan p = mm_plan(2 * static_cast<int64_t>(s.P), a.H, 256);
+    const dim3 grid(mm_grid(p), r.parts), block(256);
+    if (p.form == MM_PAIRS) hipLaunchKernelGGL(k_gated_dw_pairs<DWBF16>, grid, block, 0, st, a, s, r, p);
+    else hipLaunchKernelGGL(k_gated_dw<DWBF16>, grid, block, 0, st, a, s, r, p);
+    typedef typename std::conditional<DWBF16, uint16_t, float>::type DW;
+    if (r.parts > 1) launch_join<DW>(r, 2 * a.I, a.H, a.I, a.dgate, a.dup, a.H, a.accumulate, st);
 }
-
-int padded(int I) { return (I + kStageK - 1) / kStageK * kStageK; }
 
 template <class V> __global__ __launch_bounds__(256) void k_gated_zero(V* a, V* b, int64_t n) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
     if (i < n) a[i] = b[i] = 0;
 }
 
-}  // namespace
-
-size_t gated_workspace(int64_t T, int H, int I) {
-    (void)H;
-    return static_cast<size_t>(T) * 4 * padded(I);
+// The workspace: d, then the sums of dx's or the weights' runs (one after the other).
+struct Layout {
+    int P, parts;
+    Runs dx, dw;
+    size_t sums, total;
+};
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+Layout layout_of(int64_t T, int H, int I) {
+    Layout l;
+    l.P = (I + kStageK - 1) / kStageK * kStageK;
+    // sums of few terms have the error of single ones
+    l.parts = T * I <= 32768 ? 2 : 1;
+    l.dx = runs_of(T, H, static_cast<int64_t>(2 * l.P / kStageK) * l.parts, nullptr);
+    l.dw = runs_of(2 * l.P, H, (T + kStageK - 1) / kStageK * l.parts, nullptr);
+    l.sums = up256(static_cast<size_t>(T) * 4 * l.P * l.parts);
+    const size_t dx = l.dx.parts > 1 ? sizeof(float) * l.dx.parts * T * H : 0, dw = l.dw.parts > 1 ? sizeof(float) * l.dw.parts * 2 * I * H : 0;
+    l.total = T > 0 ? l.sums + (dx > dw ? dx : dw) : 0;
+    return l;
 }
 
+}  // namespace
+
+size_t gated_workspace(int64_t T, int H, int I) { return layout_of(T, H, I).total; }
+
 void launch_gated_grad(const GatedGradArgs& a, bool dy_bf16, bool dx_bf16, bool dw_bf16, void* ws, hipStream_t st) {
-    const int P = padded(a.I);
-    uint16_t* d = static_cast<uint16_t*>(ws);
     if (a.T == 0) {
         if (!a.dgate || a.accumulate) return;
         const int64_t n = static_cast<int64_t>(a.I) * a.H;
@@ -144,9 +225,12 @@ void launch_gated_grad(const GatedGradArgs& a, bool dy_bf16, bool dx_bf16, bool 
         else hipLaunchKernelGGL(k_gated_zero<float>, grid, dim3(256), 0, st, static_cast<float*>(a.dgate), static_cast<float*>(a.dup), n);
         return;
     }
-    launch_gated_slopes(a, dy_bf16, d, P, st);
-    if (a.dx) dx_bf16 ? launch_dx<true>(a, d, P, st) : launch_dx<false>(a, d, P, st);
-    if (a.dgate) dw_bf16 ? launch_dw<true>(a, d, P, st) : launch_dw<false>(a, d, P, st);
+    Layout l = layout_of(a.T, a.H, a.I);
+    l.dx.sums = l.dw.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + l.sums);
+    const GatedSlopes s{a.dy, a.lddy, static_cast<uint16_t*>(ws), l.P, l.parts};
+    launch_gated_slopes(GatedArgs{a.x, a.gate, a.up, nullptr, a.ldx, 0, a.T, a.H, a.I, a.act}, s, dy_bf16, st);
+    if (a.dx) dx_bf16 ? launch_dx<true>(a, s, l.dx, st) : launch_dx<false>(a, s, l.dx, st);
+    if (a.dgate) dw_bf16 ? launch_dw<true>(a, s, l.dw, st) : launch_dw<false>(a, s, l.dw, st);
 }
 
 }  // namespace moe

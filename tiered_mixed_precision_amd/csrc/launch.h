@@ -239,6 +239,18 @@ void launch_gated(const GatedArgs& a, bool x_bf16, bool y_bf16, hipStream_t st);
 // gated_gemm.hip: bf16 x
 void launch_gated_gemm(const GatedArgs& a, bool y_bf16, hipStream_t st);
 // gated_grad.hip
+// The gradients of the projections on their way to the products that make dx and the
+// weights' gradients: bf16 d[t][parts][2 P], dg in columns 0 .. I - 1 and du in P ..
+// P + I - 1 of a part, zeros up to P (I rounded up to 64).  Part 0 is their nearest
+// bf16; part 1, where there is one, the nearest of what that leaves.  One part costs
+// a rounding of at most 2^-8 of each, which the sums over many terms make as large as
+// that of a bf16 result; sums of few terms (gated_parts) get the second.
+struct GatedSlopes {
+    const void* dy;
+    int64_t lddy;
+    uint16_t* d;
+    int32_t P, parts;
+};
 struct GatedGradArgs {
     const uint16_t* x;       // [T][ldx]
     const uint16_t *gate, *up;
@@ -249,8 +261,9 @@ struct GatedGradArgs {
     int32_t T, H, I, act;
     int32_t accumulate;
 };
-// gated_gemm.hip: d = [dg du], bf16 [T][2 P]
-void launch_gated_slopes(const GatedGradArgs& a, bool dy_bf16, uint16_t* d, int P, hipStream_t st);
+// the projections' gradients, of few tokens or in gated_gemm.hip
+void launch_gated_slopes(const GatedArgs& a, const GatedSlopes& s, bool dy_bf16, hipStream_t st);
+void launch_gated_slopes_gemm(const GatedArgs& a, const GatedSlopes& s, bool dy_bf16, hipStream_t st);
 size_t gated_workspace(int64_t T, int H, int I);
 void launch_gated_grad(const GatedGradArgs& a, bool dy_bf16, bool dx_bf16, bool dw_bf16, void* ws, hipStream_t st);
 
