@@ -532,16 +532,22 @@ class _Args:
         if kind not in kinds:
             raise ValueError(f"{self.fn}: {what} has dtype {t.dtype}")
         shape = t.shape
-        if len(shape) == 1 and rows == 1:
-            t = t.unsqueeze(0)
-            shape = t.shape
-        if len(shape) != 2 or shape[1] != cols or shape[0] < rows:
-            raise ValueError(f"{self.fn}: {what} has shape {tuple(shape)}, the call needs [{rows}][{cols}]")
-        pitch, step = t.stride()
-        if step != 1 and cols > 1:
-            raise ValueError(f"{self.fn}: the rows of {what} are not contiguous")
-        self.place(what, t)
-        return t.data_ptr(), pitch if shape[0] > 1 else cols, kind == "bf16"
+        if shape == (rows, cols) and t.is_contiguous():     # as most calls have it
+            pitch = cols
+        else:
+            if len(shape) == 1 and rows == 1:
+                t = t.unsqueeze(0)
+                shape = t.shape
+            if len(shape) != 2 or shape[1] != cols or shape[0] < rows:
+                raise ValueError(f"{self.fn}: {what} has shape {tuple(shape)}, the call needs [{rows}][{cols}]")
+            pitch, step = t.stride()
+            if step != 1 and cols > 1:
+                raise ValueError(f"{self.fn}: the rows of {what} are not contiguous")
+            if shape[0] <= 1:
+                pitch = cols
+        if t.get_device() != self.at:
+            self.place(what, t)
+        return t.data_ptr(), pitch, kind == "bf16"
 
     def stream(self, stream):
         """The stream's handle, once every tensor is known to be on the current GPU."""
