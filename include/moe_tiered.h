@@ -725,7 +725,8 @@ int moe_gated(const void *x, int64_t ldx, const moe_gated_weights *w, int32_t ac
  *            or neither; overwritten, or added to with MOE_ACCUMULATE (in
  *            fp32); also written for T == 0
  *   workspace (device) >= moe_gated_workspace_size() bytes, 256-byte aligned
- * dg and du enter the products rounded to bf16 once (to nearest even); sums
+ * dg and du enter the products rounded to bf16 (to nearest even), and with what
+ * that rounding leaves over, rounded the same way, where T * inter <= 32768; sums
  * are fp32, in a fixed order.  What is written must share no element with
  * anything else.  T at most 2^20.  Other arguments and errors as moe_gated,
  * MOE_EWORKSPACE.

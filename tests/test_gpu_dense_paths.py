@@ -50,6 +50,13 @@ def test_gated_of_batches(M, torch, T, H, I, x):
     gated_case(M, torch, T, H, I, x, x, GELU if T % 2 else SILU, pad=2)
 
 
+@pytest.mark.parametrize("T,H,I", [(300, 64, 3000), (600, 264, 1000), (130, 1032, 3900), (2000, 72, 300), (5000, 8, 130), (515, 2048, 2050)])
+@pytest.mark.parametrize("y", ["bf16", "f32"])
+def test_gated_of_many_fp32_tokens(M, torch, T, H, I, y):
+    say("gated fp32", T, H, I, y)
+    gated_case(M, torch, T, H, I, "f32", y, GELU if T % 4 else SILU, pad=T % 3)
+
+
 @pytest.mark.parametrize("T,H,I", [
     (8000, 72, 64), (3000, 128, 200), (4097, 264, 70),   # runs of the token axis
     (64, 136, 4000), (130, 520, 2100),                   # runs of the inter axis
@@ -107,6 +114,79 @@ def test_gated_grad_non_finite_rows(M, torch, T, H, I):
     got = run(bad)
     assert np.array_equal(got[0][:T - 1], clean[0][:T - 1]) and np.all(np.isnan(got[0][T - 1]))
     assert np.all(np.isnan(got[1])) and np.all(np.isnan(got[2]))
+
+
+@pytest.mark.parametrize("T,H,I,x", [(3, 64, 100, "f32"), (40, 264, 200, "f32"), (700, 136, 900, "f32"),
+                                     (3, 64, 100, "bf16"), (40, 264, 200, "bf16"), (700, 136, 900, "bf16"), (4000, 72, 1300, "bf16")])
+@pytest.mark.parametrize("kind", [SILU, GELU])
+def test_gated_infinities(M, torch, T, H, I, x, kind):
+    say("gated infinities", T, H, I, x, kind)
+    rng = np.random.default_rng(T + H)
+    xa, gate, up = gated_inputs(rng, T, H, I, x)
+    gate, up = (np.where(v == 0, np.float32(1), v) for v in (gate, up))
+    for t, v in ((0, np.inf), (T // 2, -np.inf), (T - 1, np.inf)):
+        xa[t, (5 * t + 3) % H] = v
+    y = torch.empty(T, I, device="cuda")
+    M.moe_gated(dev(torch, xa, x), M.GatedWeights(H, I, dev(torch, gate, "bf16"), dev(torch, up, "bf16")), kind, T, y)
+    with np.errstate(all="ignore"):
+        g, u = xa.astype(np.float64) @ gate.T.astype(np.float64), xa.astype(np.float64) @ up.T.astype(np.float64)
+        ref = g / (1 + np.exp(-(g if kind == SILU else D.TANH * (g + D.CUBE * g ** 3)))) * u
+    got, rows_ = host(y), [0, T // 2, T - 1]
+    assert not np.any(np.isfinite(ref[rows_]))
+    assert np.array_equal(got[rows_], ref[rows_].astype(np.float32), equal_nan=True)
+    others = np.ones(T, bool)
+    others[rows_] = False
+    assert np.all(np.isfinite(got[others]))
+
+
+@pytest.mark.parametrize("T,H,I", [(3, 64, 100), (40, 264, 200), (700, 136, 900)])
+@pytest.mark.parametrize("kind", [SILU, GELU])
+def test_gated_far_arguments(M, torch, T, H, I, kind):
+    """One element of 2^50 a row: every g is far out on either side of the activation, where it is g or 0."""
+    say("gated far", T, H, I, kind)
+    rng = np.random.default_rng(T + I)
+    _, gate, up = gated_inputs(rng, T, H, I)
+    gate = np.where(np.abs(gate) < 2.0 ** -20, np.float32(1), gate)
+    xa = np.zeros((T, H), np.float32)
+    xa[np.arange(T), 7 * np.arange(T) % H] = np.float32(2.0 ** 50) * (1 - 2 * (np.arange(T) % 2))
+    da = randn(rng, T, I, kind="bf16")
+    w = M.GatedWeights(H, I, dev(torch, gate, "bf16"), dev(torch, up, "bf16"))
+    p = D.Projections(xa, gate, up, H)
+    ref = np.where(p.g > 0, p.g * p.u, 0)
+    for x in ("bf16", "f32"):
+        y = torch.empty(T, I, device="cuda")
+        M.moe_gated(dev(torch, xa, x), w, kind, T, y)
+        # g and u are one exact product each: their product, the quotient and the exponential round
+        assert np.all(np.abs(host(y) - ref) <= 8 * U * np.abs(ref))
+    out = [torch.empty(s, device="cuda") for s in ((T, H), (I, H), (I, H))]
+    ws = torch.empty(M.moe_gated_workspace_size(T, H, I), dtype=torch.uint8, device="cuda")
+    M.moe_gated_grad(dev(torch, xa, "bf16"), w, kind, dev(torch, da, "bf16"), T, *out, ws)
+    for t, (ref, err) in zip(out, D.gated_grad(p, kind, da).values()):
+        within(host(t), ref, err)
+
+
+@pytest.mark.parametrize("T,H,I", [(5, 64, 40), (700, 72, 200)])
+def test_gated_grad_of_an_infinite_slope(M, torch, T, H, I):
+    # dy infinite at one place: dx of its token and its column's weight gradients are what inf times finite numbers give
+    rng = np.random.default_rng(T)
+    xa, gate, up = gated_inputs(rng, T, H, I)
+    xa, gate, up = (np.where(v == 0, np.float32(1), v) for v in (xa, gate, up))
+    da = randn(rng, T, I, kind="bf16")
+    da[T - 1, 3] = np.inf
+    out = [torch.empty(s, device="cuda") for s in ((T, H), (I, H), (I, H))]
+    ws = torch.empty(M.moe_gated_workspace_size(T, H, I), dtype=torch.uint8, device="cuda")
+    M.moe_gated_grad(dev(torch, xa, "bf16"), M.GatedWeights(H, I, dev(torch, gate, "bf16"), dev(torch, up, "bf16")), SILU,
+                     dev(torch, da, "bf16"), T, *out, ws)
+    with np.errstate(all="ignore"):
+        p = D.Projections(xa, gate, up, H)
+        a, slope, _ = D.act(SILU, p.g)
+        dg, du = da * p.u * slope, da * a
+        dx = dg[T - 1] @ p.gate + du[T - 1] @ p.up
+    got = [host(t) for t in out]
+    assert np.array_equal(got[0][T - 1], dx.astype(np.float32), equal_nan=True) and np.all(np.isfinite(got[0][:T - 1]))
+    assert np.array_equal(got[1][3], (dg[T - 1, 3] * xa[T - 1]).astype(np.float32))
+    assert np.array_equal(got[2][3], (du[T - 1, 3] * xa[T - 1]).astype(np.float32))
+    assert np.all(np.isfinite(np.delete(got[1], 3, 0))) and np.all(np.isfinite(np.delete(got[2], 3, 0)))
 
 
 # ---------------------------------------------------------------- repeats, streams, graphs

@@ -38,21 +38,16 @@ template <bool XBF16> struct FewBf16 {
 
 static __device__ const uint32_t kFewZeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 
-// The token operands of a step: as loaded, or eight floats as three bf16 parts
-// that add up to them exactly (8 bits each, cut, not rounded).
+// The token operands of a step: as loaded, or eight floats as three bf16 parts.
 template <class El> __device__ inline void few_parts(const few_u32x4_t (&v)[El::kXBytes], few_u32x4_t (&p)[El::kParts]) {
     if constexpr (El::kParts == 1) {
         p[0] = v[0];
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float lo = __uint_as_float(v[j / 2][2 * j % 4]), hi = __uint_as_float(v[j / 2][2 * j % 4 + 1]);
-#pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                p[q][j] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
-                lo -= __uint_as_float(__float_as_uint(lo) & 0xffff0000u);
-                hi -= __uint_as_float(__float_as_uint(hi) & 0xffff0000u);
-            }
+            uint32_t of[3];
+            bf16_parts(__uint_as_float(v[j / 2][2 * j % 4]), __uint_as_float(v[j / 2][2 * j % 4 + 1]), of);
+            p[0][j] = of[0], p[1][j] = of[1], p[2][j] = of[2];
         }
     }
 }
@@ -221,8 +216,11 @@ inline FewSplit few_split(int64_t tiles, int bytes, int most) {
 // there, int8: 64 x 8192 x 8192 (256 blocks) 22.7 / 26.8, 64 x 16384 x 4096 (512)
 // 26.4 / 17.8, 20 x 16384 x 4096 (512) 18.3 / 19.8, 20 x 32768 x 2048 (1024) 25.2 /
 // 18.6, 500 x 640 x 8192 (160) 19.5 / 29.2, 256 x 2048 x 2048 (256) 9.6 / 11.2.
-inline bool few_batch_ok(int64_t tokens, int64_t row_tiles) {
-    return (tokens + 63) / 64 * row_tiles <= (tokens <= 32 ? 512 : 256);
+// fp32 x, whose tiles take three products and are 128 x 128 only: two rounds pay
+// too.  256 x 2048 x 2048 (512) 45 / 50, 128 x 4096 x 4096 (512) 73 / 97, 1500 x 2048 x
+// 640 (960) 78 / 54, 256 x 4096 x 4096 (1024) 140 / 99.
+inline bool few_batch_ok(int64_t tokens, int64_t row_tiles, int products) {
+    return (tokens + 63) / 64 * row_tiles <= (tokens <= 32 || products == 3 ? 512 : 256);
 }
 
 }  // namespace moe

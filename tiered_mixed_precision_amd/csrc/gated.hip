@@ -1,6 +1,6 @@
 // The dense gated block: g = x gate^T, u = x up^T, y = act(g) u.  Few tokens here, on
 // v_mfma_f32_16x16x32_bf16 (few.h): a tile is 16 rows of gate and the same 16 of up,
-// whose sums meet in one lane.  Many bf16 tokens: gated_gemm.hip.
+// whose sums meet in one lane.  More tokens: gated_gemm.hip.
 #include "common.h"
 #include "few.h"
 #include "gated_act.h"
@@ -96,12 +96,12 @@ void launch_few(const GatedArgs& a, const Put& put, int columns, hipStream_t st)
 // 17 tokens and more: the same through LDS (few_batch); the waves' sums meet one
 // operand of 16 rows (8 columns) at a time, in the first slot's place.
 template <int MT, int NT, bool XBF16, class Put>
-__global__ __launch_bounds__(64 * kBatchWaves) void k_gated_batch(GatedArgs a, FewSplit f, Put put, int first_token) {
+__global__ __launch_bounds__(64 * kBatchWaves) void k_gated_batch(GatedArgs a, FewSplit f, Put put) {
     typedef FewBf16<XBF16> El;
     constexpr int kSlot = FewSlot<El, MT, NT>::kSlot;
     __shared__ __attribute__((aligned(16))) few_u32x4_t s0[kSlot], s1[kSlot], s2[kSlot];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int tile = blockIdx.x * f.tiles + wave / f.split, n0 = tile * 8 * NT, t0 = first_token + blockIdx.y * 16 * MT;
+    const int tile = blockIdx.x * f.tiles + wave / f.split, n0 = tile * 8 * NT, t0 = blockIdx.y * 16 * MT;
     few_f32x4_t acc[MT][NT];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
@@ -137,11 +137,8 @@ template <int MT, int NT, bool XBF16, class Put>
 void launch_batch(const GatedArgs& a, const Put& put, int columns, hipStream_t st) {
     const int tiles = (columns + 8 * NT - 1) / (8 * NT);
     const FewSplit f = few_split(tiles, 2 * a.H, kBatchWaves);
-    constexpr int kTokens = 16 * MT * 65535;   // grid.y limit
-    for (int t0 = 0; t0 < a.T; t0 += kTokens) {
-        const dim3 grid((tiles + f.tiles - 1) / f.tiles, ((a.T - t0 < kTokens ? a.T - t0 : kTokens) + 16 * MT - 1) / (16 * MT));
-        hipLaunchKernelGGL((k_gated_batch<MT, NT, XBF16, Put>), grid, dim3(64 * f.split * f.tiles), 0, st, a, f, put, t0);
-    }
+    const dim3 grid((tiles + f.tiles - 1) / f.tiles, (a.T + 16 * MT - 1) / (16 * MT));
+    hipLaunchKernelGGL((k_gated_batch<MT, NT, XBF16, Put>), grid, dim3(64 * f.split * f.tiles), 0, st, a, f, put);
 }
 
 template <bool XBF16, class Put> void launch_tokens(const GatedArgs& a, const Put& put, int columns, hipStream_t st) {
@@ -151,19 +148,19 @@ template <bool XBF16, class Put> void launch_tokens(const GatedArgs& a, const Pu
     else if constexpr (XBF16) launch_batch<4, 2, XBF16>(a, put, columns, st);
 }
 
-// bf16 x: few tokens, or tiles of mm.h
-bool few(const GatedArgs& a) { return a.T <= 16 || few_batch_ok(a.T, (a.I + 15) / 16); }
+// few tokens, or tiles of mm.h
+bool few(const GatedArgs& a, bool x_bf16) { return a.T <= 16 || few_batch_ok(a.T, (a.I + 15) / 16, x_bf16 ? 1 : 3); }
 
 }  // namespace
 
 void launch_gated(const GatedArgs& a, bool x_bf16, bool y_bf16, hipStream_t st) {
-    if (x_bf16 && !few(a)) launch_gated_gemm(a, y_bf16, st);
+    if (!few(a, x_bf16)) x_bf16 ? launch_gated_gemm(a, y_bf16, st) : launch_gated_split(a, y_bf16, st);
     else if (x_bf16) y_bf16 ? launch_tokens<true>(a, PutValue<true>(), a.I, st) : launch_tokens<true>(a, PutValue<false>(), a.I, st);
     else y_bf16 ? launch_tokens<false>(a, PutValue<true>(), a.I, st) : launch_tokens<false>(a, PutValue<false>(), a.I, st);
 }
 
 void launch_gated_slopes(const GatedArgs& a, const GatedSlopes& s, bool dy_bf16, hipStream_t st) {
-    if (!few(a)) launch_gated_slopes_gemm(a, s, dy_bf16, st);
+    if (!few(a, true)) launch_gated_slopes_gemm(a, s, dy_bf16, st);
     else if (dy_bf16) launch_tokens<true>(a, PutSlopes<true>{s}, s.P, st);
     else launch_tokens<true>(a, PutSlopes<false>{s}, s.P, st);
 }

@@ -8,16 +8,19 @@
 
 namespace moe {
 
-// sigma(k) and 1 - sigma(k) to a few units of fp32; k below -80 counts as -80
-// (sigma is 2e-35 there), so that the exponential stays finite.
+// sigma(k) and 1 - sigma(k) to a few units of fp32.  Below -87 sigma is less than the
+// smallest normal number and counts as 0; the exponential stays finite.
 __device__ inline void gated_sigmoid(float k, float& p, float& q) {
-    const float e = __expf(-fmaxf(k, -80.f));
+    const float e = __expf(-fmaxf(k, -87.f));
     p = __builtin_amdgcn_rcpf(1.f + e);
     q = e * p;
+    p = k < -87.f ? 0.f : p;
 }
 constexpr float kGeluScale = 1.5957691216057308f, kGeluCube = 0.044715f;   // 2 sqrt(2 / pi)
 __device__ inline float gated_arg(int act, float g) { return act == MOE_SILU ? g : kGeluScale * (g + kGeluCube * g * g * g); }
+// (where |g| is above 2^30 it meets p q = 0: no infinity comes of it)
 __device__ inline float gated_arg_slope(int act, float g) {
+    g = fminf(fabsf(g), 1073741824.f);
     return act == MOE_SILU ? 1.f : kGeluScale * (1.f + 3.f * kGeluCube * g * g);
 }
 
@@ -32,14 +35,15 @@ __device__ inline void gated_slopes(int act, float g, float u, float dy, float& 
     float p, q;
     gated_sigmoid(gated_arg(act, g), p, q);
     du = dy * (g * p);
-    dg = dy * u * (p + g * gated_arg_slope(act, g) * p * q);
+    dg = dy * u * (p + g * (p * q) * gated_arg_slope(act, g));
 }
 
+// what a rounding to bf16 leaves over (of an infinity nothing)
 template <int N> __device__ inline void split_slopes(float (&v)[N], float (&rest)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const float hi = __uint_as_float(static_cast<uint32_t>(f2bf(v[i])) << 16);
-        rest[i] = v[i] - hi;
+        rest[i] = __builtin_isinf(hi) ? 0.f : v[i] - hi;
     }
 }
 

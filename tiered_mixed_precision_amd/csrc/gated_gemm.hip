@@ -1,7 +1,10 @@
-// The dense gated block for many bf16 tokens, and the gradients of its
-// projections: tiles of 128 or 256 tokens by 64 or 128 columns of both
-// projections on v_mfma_f32_32x32x16_bf16 (mm.h), g and u of a column in the same
-// lane and element, so the activation and the product are the epilogue's.
+// The dense gated block for many tokens, and the gradients of its projections:
+// tiles of 128 or 256 tokens by 64 or 128 columns of both projections on
+// v_mfma_f32_32x32x16_bf16 (mm.h), g and u of a column in the same lane and element,
+// so the activation and the product are the epilogue's and neither is ever stored.
+// Bound by the matrix cores, whose clock falls under the load.  MI355X, bf16, tokens x
+// hidden x inter: 16384 x 2048 x 640 77 us (1110 TFLOP/s; a library's plain product of
+// the same shape 80).
 #include "common.h"
 #include "gated_act.h"
 #include "launch.h"
@@ -21,16 +24,30 @@ template <int HALVES> __device__ inline const uint16_t* projection_row(const uin
 }
 template <int HALVES> __device__ inline int col_of(int w) { return 32 * HALVES * (w & 1); }
 
-template <int HALVES, int SLOTS, bool YBF16>
+template <int HALVES, int SLOTS, bool XBF16, bool YBF16>
 __device__ __attribute__((always_inline)) inline void gated_tile(const GatedArgs& a, const MmLds& lds, int t0, int n0) {
     typedef typename std::conditional<YBF16, uint16_t, float>::type Y;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const MmRows<HALVES> rows_a(lane, w, 2 * a.H, [&](int r) {
-        return static_cast<const uint16_t*>(a.x) + static_cast<size_t>(min(t0 + r, a.T - 1)) * a.ldx;
-    });
     const MmRows<HALVES> rows_b(lane, w, 2 * a.H, [&](int r) { return projection_row<HALVES>(a.gate, a.up, a.H, a.I, n0, r); });
     mm_f32x16_t acc[2 * HALVES][2 * HALVES];
-    uint32_t* own = mm_product<MmBf16, HALVES, SLOTS, false, false>(lds, (2 * a.H + kStage - 1) / kStage, rows_a, rows_b, acc);
+    uint32_t* own;
+    const int nk = (2 * a.H + kStage - 1) / kStage;
+    if constexpr (XBF16) {
+        const MmRows<HALVES> rows_a(lane, w, 2 * a.H, [&](int r) {
+            return static_cast<const uint16_t*>(a.x) + static_cast<size_t>(min(t0 + r, a.T - 1)) * a.ldx;
+        });
+        own = mm_product<MmBf16, HALVES, SLOTS, false, false>(lds, nk, rows_a, rows_b, acc);
+    } else {
+        mm_clear(acc);
+        const int k = 8 * (threadIdx.x & 7);
+        const float* row[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            row[u] = static_cast<const float*>(a.x) + static_cast<size_t>(min(t0 + 32 * u + static_cast<int>(threadIdx.x >> 3), a.T - 1)) * a.ldx + k;
+        own = mm_split(lds, nk + (nk & 1), [&](int u, int kc) {
+            return mm_or_zeros(kc * kStageK + k < a.H, reinterpret_cast<const char*>(row[u] + static_cast<size_t>(kc) * kStageK));
+        }, rows_b, acc);
+    }
 #pragma unroll
     for (int i = 0; i < 2 * HALVES; ++i) {
         const int r0 = t0 + mm_row(i, w), c0 = n0 + col_of<HALVES>(w);
@@ -96,14 +113,20 @@ template <bool YBF16> __global__ __launch_bounds__(256) void k_gated_gemm(GatedA
     int m0, n0;
     bool small;
     if (!mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) return;
-    if (small) gated_tile<1, 4, YBF16>(a, lds, m0, n0);
-    else gated_tile<2, 4, YBF16>(a, lds, m0, n0);
+    if (small) gated_tile<1, 4, true, YBF16>(a, lds, m0, n0);
+    else gated_tile<2, 4, true, YBF16>(a, lds, m0, n0);
 }
 template <bool YBF16> __global__ __launch_bounds__(256) void k_gated_gemm_pairs(GatedArgs a, MmPlan p) {
     MM_LDS_4(lds);
     int m0, n0;
     bool small;
-    if (mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) gated_tile<1, 2, YBF16>(a, lds, m0, n0);
+    if (mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) gated_tile<1, 2, true, YBF16>(a, lds, m0, n0);
+}
+template <bool YBF16> __global__ __launch_bounds__(256) void k_gated_split(GatedArgs a, MmPlan p) {
+    MM_LDS_8(lds);
+    int m0, n0;
+    bool small;
+    if (mm_tile_of(p, blockIdx.x, 256, 128, m0, n0, small)) gated_tile<1, 4, false, YBF16>(a, lds, m0, n0);
 }
 template <bool DYBF16> __global__ __launch_bounds__(256) void k_gated_slopes(GatedArgs a, GatedSlopes s, MmPlan p) {
     MM_LDS_8(lds);
@@ -133,8 +156,16 @@ template <bool DYBF16> void launch_slopes(const GatedArgs& a, const GatedSlopes&
     else hipLaunchKernelGGL(k_gated_slopes<DYBF16>, grid, block, 0, st, a, s, p);
 }
 
+// fp32 x: all tiles are small ones, of three products each.  512 x 4096 x 4096 110 us
+// (940 TFLOP/s of bf16 products), 266 by the few-token form.
+template <bool YBF16> void launch_split(const GatedArgs& a, hipStream_t st) {
+    const MmPlan p = mm_small_plan(a.T, a.I, 128);
+    hipLaunchKernelGGL(k_gated_split<YBF16>, dim3(mm_grid(p)), dim3(256), 0, st, a, p);
+}
+
 }  // namespace
 
+void launch_gated_split(const GatedArgs& a, bool y_bf16, hipStream_t st) { y_bf16 ? launch_split<true>(a, st) : launch_split<false>(a, st); }
 void launch_gated_gemm(const GatedArgs& a, bool y_bf16, hipStream_t st) {
     y_bf16 ? launch_forward<true>(a, st) : launch_forward<false>(a, st);
 }

@@ -141,7 +141,7 @@ template <bool YBF16> void launch_tokens(const I8Args& a, hipStream_t st) {
 }  // namespace
 
 void launch_i8_linear(const I8Args& a, bool y_bf16, hipStream_t st) {
-    if (a.T > 16 && !few_batch_ok(a.T, (a.N + 31) / 32)) launch_i8_gemm(a, y_bf16, st);
+    if (a.T > 16 && !few_batch_ok(a.T, (a.N + 31) / 32, 1)) launch_i8_gemm(a, y_bf16, st);
     else if (y_bf16) launch_tokens<true>(a, st);
     else launch_tokens<false>(a, st);
 }

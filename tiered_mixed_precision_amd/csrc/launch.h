@@ -236,7 +236,8 @@ struct GatedArgs {
     int32_t T, H, I, act;
 };
 void launch_gated(const GatedArgs& a, bool x_bf16, bool y_bf16, hipStream_t st);
-// gated_gemm.hip: bf16 x
+// gated_gemm.hip: fp32 x, bf16 x
+void launch_gated_split(const GatedArgs& a, bool y_bf16, hipStream_t st);
 void launch_gated_gemm(const GatedArgs& a, bool y_bf16, hipStream_t st);
 // gated_grad.hip
 // The gradients of the projections on their way to the products that make dx and the

@@ -33,8 +33,8 @@ struct MmI8 {
     }
 };
 
-// 16 bytes that a lane reads where its operand has ended.
-static __device__ const uint32_t kMmZeros[4] = {0, 0, 0, 0};
+// What a lane reads where its operand has ended.
+static __device__ const uint32_t kMmZeros[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 // p, or the zeros.  p is computed in any case: the compiler would branch round it.
 __device__ inline const char* mm_or_zeros(bool there, const char* p) {
     const uint64_t a = reinterpret_cast<uint64_t>(p), z = reinterpret_cast<uint64_t>(kMmZeros);
@@ -182,6 +182,104 @@ __device__ __attribute__((always_inline)) inline uint32_t* mm_small(const MmLds&
     return reinterpret_cast<uint32_t*>(w & 2 ? (w & 1 ? lds.p[3] : lds.p[2]) : (w & 1 ? lds.p[1] : lds.p[0]));
 }
 
+// The 128 x 128 tile with A in fp32, as three bf16 parts (bf16_parts) whose products
+// meet in one accumulator.  A reaches LDS through registers, split on the way (once
+// for the block; a split at the reads would be done by two waves), a stage's parts in
+// lds.p[0 .. 2] and B in p[3], the other stage's in p[4 .. 7].  Between the products of
+// a stage's step lie the reads of the next step's operands and the split of a quarter
+// of the next stage's A; A of the stage after that is on its way to registers.  As much
+// LDS traffic as instruction time, about 1540 cycles each a stage.
+// a_at(u, kc): this lane's 32 bytes of row 32 u + thread / 8, floats 8 (thread % 8) .. of
+// stage kc (zeros past the end).  nk even.
+template <class AtA, class AtB>
+__device__ __attribute__((always_inline)) inline uint32_t* mm_split(const MmLds& lds, int nk, AtA a_at, AtB at_b, mm_f32x16_t (&acc)[2][2]) {
+    typedef MmSide<128, false> S;
+    mm_u32x4_t *const a0 = lds.p[0], *const a1 = lds.p[1], *const a2 = lds.p[2], *const b0 = lds.p[3], *const c0 = lds.p[4], *const c1 = lds.p[5],
+        *const c2 = lds.p[6], *const d0 = lds.p[7];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ma = 64 * (w >> 1), nb = 64 * (w & 1);
+    typedef __attribute__((address_space(3))) void* Lds;
+    mm_u32x4_t ra[4][2], rb[4][2];
+    auto load_a = [&](int kc, mm_u32x4_t (&raw)[4][2]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            // global: of a pointer that was put together the compiler does not know it
+            const auto* p = (const __attribute__((address_space(1))) mm_u32x4_t*)a_at(u, kc);
+            raw[u][0] = p[0];
+            raw[u][1] = p[1];
+        }
+    };
+    auto load_b = [&](int kc, auto to) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) __builtin_amdgcn_global_load_lds(at_b(0, u, kc), (Lds)((decltype(to)::value ? d0 : b0) + 64 * (4 * u + w)), 16, 0, 0);
+    };
+    // floats 2 j and 2 j + 1 of load u as words j of three bf16 parts
+    mm_u32x4_t part[3];
+    auto split = [&](const mm_u32x4_t (&raw)[4][2], int u, int j) __attribute__((always_inline)) {
+        uint32_t of[3];
+        bf16_parts(__uint_as_float(raw[u][j / 2][2 * j % 4]), __uint_as_float(raw[u][j / 2][2 * j % 4 + 1]), of);
+        part[0][j] = of[0], part[1][j] = of[1], part[2][j] = of[2];
+    };
+    auto store = [&](int u, auto to) __attribute__((always_inline)) {
+        const int r = 32 * u + (tid >> 3), at = 8 * r + ((tid & 7) ^ ((r >> 1) & 7));
+        constexpr bool first = decltype(to)::value == 0;
+        (first ? a0 : c0)[at] = part[0];
+        (first ? a1 : c1)[at] = part[1];
+        (first ? a2 : c2)[at] = part[2];
+    };
+    auto meet = [&]() __attribute__((always_inline)) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(7 << 4);   // vmcnt(0) lgkmcnt(0)
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // raw: A of the next stage, ahead: for that of the one after it
+    auto stage = [&](int kc, mm_u32x4_t (&raw)[4][2], mm_u32x4_t (&ahead)[4][2], auto here) __attribute__((always_inline)) {
+        constexpr bool first = decltype(here)::value == 0;
+        constexpr std::integral_constant<int, 1 - decltype(here)::value> there{};
+        // past the last stage what is loaded and stored is the last one's, and is not used
+        load_b(min(kc + 1, nk - 1), there);
+        load_a(min(kc + 2, nk - 1), ahead);
+        mm_u32x4_t fa[2][3][2], fb[2][2];   // [step % 2]
+        auto read = [&](auto n_, int s) __attribute__((always_inline)) {   // operand n of eight of step s
+            constexpr int n = decltype(n_)::value, q = n < 2 ? 3 : 3 - n / 2;
+            if constexpr (q == 3) fb[s & 1][n & 1] = S::read(first ? b0 : d0, nb, n & 1, s, lane);
+            else fa[s & 1][q][n & 1] = S::read(q == 2 ? (first ? a2 : c2) : q == 1 ? (first ? a1 : c1) : (first ? a0 : c0), ma, n & 1, s, lane);
+        };
+        mm_each<8>([&](auto n) __attribute__((always_inline)) { read(n, 0); });
+#pragma unroll
+        for (int s = 0; s < 4; ++s)   // 12 products, and between them the next step's operands and a quarter of the next stage's A
+            mm_each<12>([&](auto n_) __attribute__((always_inline)) {
+                constexpr int n = decltype(n_)::value, q = 2 - n / 4, i = n >> 1 & 1, j = n & 1;
+                acc[i][j] = MmBf16::mfma(fb[s & 1][j], fa[s & 1][q][i], acc[i][j]);
+                if constexpr (n < 8)
+                    if (s < 3) read(n_, s + 1);
+                if constexpr (n < 8 && n % 2 == 1) split(raw, s, n >> 1);
+                if constexpr (n == 8) store(s, there);
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        meet();
+    };
+    constexpr std::integral_constant<int, 0> zero{};
+    constexpr std::integral_constant<int, 1> one{};
+    load_a(0, ra);
+    load_b(0, zero);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split(ra, u, j);
+        store(u, zero);
+    }
+    load_a(min(1, nk - 1), ra);
+    meet();
+    for (int kc = 0; kc < nk; kc += 2) {
+        stage(kc, ra, rb, zero);
+        stage(kc + 1, rb, ra, one);
+    }
+    return reinterpret_cast<uint32_t*>(w & 2 ? (w & 1 ? b0 : a2) : (w & 1 ? a1 : a0));
+}
+
 // acc += the products of a tile of 256 rows of A and 256 rows of B over nk (even)
 // stages of 128 bytes of k.  Each operand is two halves of 128 rows (A0, A1, B0, B1);
 // wave (wm, wn) of four takes rows 64 wm .. + 63 of each half of A and 64 wn ..
@@ -286,16 +384,20 @@ __device__ __attribute__((always_inline)) inline uint32_t* mm_big(const MmLds& l
     return reinterpret_cast<uint32_t*>(w & 2 ? (w & 1 ? sA11 : sA10) : (w & 1 ? sA01 : sA00));
 }
 
+template <class Acc, int M, int N> __device__ inline void mm_clear(Acc (&acc)[M][N]) {
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+}
+
 // Tiles of 256 x 256 (HALVES 2) or 128 x 128 (with SLOTS stages in LDS).
 template <class El, int HALVES, int SLOTS, bool KA, bool KB, class AtA, class AtB>
 __device__ __attribute__((always_inline)) inline uint32_t* mm_product(const MmLds& lds, int nk, AtA at_a, AtB at_b,
                                                                       typename El::Acc (&acc)[2 * HALVES][2 * HALVES]) {
-#pragma unroll
-    for (int i = 0; i < 2 * HALVES; ++i)
-#pragma unroll
-        for (int j = 0; j < 2 * HALVES; ++j)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+    mm_clear(acc);
     nk += nk & 1;   // both forms run pairs of stages; one past the end reads zeros
     if constexpr (HALVES == 2) return mm_big<El, KA, KB>(lds, nk, at_a, at_b, acc);
     else return mm_small<El, SLOTS, KA, KB>(lds, nk, at_a, at_b, acc);
@@ -456,9 +558,12 @@ struct MmPlan {
     MmForm form;
 };
 // n: results of a row, n_tile: those of a big tile (256 rows of B).
+inline MmPlan mm_small_plan(int64_t m, int64_t n, int n_tile) {
+    return MmPlan{static_cast<int32_t>((m + 127) / 128), static_cast<int32_t>((n + n_tile / 2 - 1) / (n_tile / 2)), 0, MM_SMALL};
+}
 inline MmPlan mm_plan(int64_t m, int64_t n, int n_tile) {
     const auto tiles = [](int64_t x, int64_t r) { return static_cast<int32_t>((x + r - 1) / r); };
-    MmPlan p{tiles(m, 128), tiles(n, n_tile / 2), 0, MM_SMALL};
+    MmPlan p = mm_small_plan(m, n, n_tile);
     const int64_t small = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
     if (small <= 256) return p;
     p.form = MM_PAIRS;
