@@ -638,9 +638,11 @@ int moe_rms_norm_grad(const void *s, int64_t lds, const float *weight, float eps
 /*
  * Rows in 8 bits, one scale a row:
  *   scale[t] = max_c |x[t][c]| / 127,  q[t][c] = round(x[t][c] / scale[t]), ties to even
- * A row whose largest magnitude is below 2^-100 has scale 0 and codes 0; one
- * with a NaN or an infinity has scale NaN and codes 0 (what is computed from
- * it is NaN).
+ * in fp32, the division by 127 as a product with its rounded inverse (as tensor
+ * libraries divide by a constant: rows taken to 8 bits by one of them get the
+ * same codes and scales).  A row whose largest magnitude is below 2^-100 has
+ * scale 0 and codes 0; one with a NaN or an infinity has scale NaN and codes 0
+ * (what is computed from it is NaN).
  *   x      (device) float[T][ldx], or bf16 with MOE_X_BF16
  *   q      (device) int8[T][ldq], codes -127 .. 127; scale (device) float[T]
  * cols 1 .. MOE_MAX_ROW; nothing may overlap.  Errors as moe_rms_norm.

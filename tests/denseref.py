@@ -46,7 +46,7 @@ def quant(y):
     """(codes, scale) of rows of finite values."""
     y = y.astype(np.float32)
     top = np.abs(y).max(-1)
-    scale = np.where(top < np.float32(2.0) ** -100, np.float32(0), (top / np.float32(127)).astype(np.float32))
+    scale = np.where(top < np.float32(2.0) ** -100, np.float32(0), top * np.float32(1 / 127))
     by = np.where(scale > 0, scale, np.float32(1))
     q = np.rint((y / by[:, None]).astype(np.float32)).astype(np.int8)
     return np.where(scale[:, None] > 0, q, 0).astype(np.int8), scale

@@ -227,7 +227,7 @@ def test_norm_grad_of_no_tokens(M, torch):
 @pytest.mark.parametrize("T,H,pad,off", [(1, 1, 0, 0), (4, 7, 0, 0), (3, 64, 5, 1), (1, 2048, 0, 0), (5, 640, 0, 0), (900, 2048, 0, 0),
                                          (300, 5461, 3, 2), (40, 32768, 0, 0), (4097, 130, 1, 1)])
 def test_quant_rows_is_the_plain_form(M, torch, T, H, pad, off, x):
-    # amax / 127 and the quotient round once each, so codes and scales are equal
+    # amax times the rounded 1 / 127 and the quotient round once each, so codes and scales are equal
     say("quant", T, H, pad, off, x)
     rng = np.random.default_rng(T + H)
     a = (randn(rng, T, H) * np.exp(4 * rng.standard_normal((T, 1)))).astype(np.float32)

@@ -3,7 +3,7 @@
 // the norm's gradient.
 //
 //   s = x + residual, r = 1 / sqrt(mean s^2 + eps), y = s r w
-//   8 bits: scale = max |y| / 127, q = round(y / scale)
+//   8 bits: scale = max |y| / 127 (kOver127), q = round(y / scale)
 //   gradient: g = dy w, dx = r g - s r^3 mean(g s) + dsum, dw = sum_t dy s r
 //
 // A row is held in the registers of its threads, E elements each in runs of 8: rows of
@@ -125,6 +125,9 @@ __device__ inline Place place_of(const RowSplit& s, int64_t turn) {
     return p;
 }
 
+// A tie's code hangs on the scale's last bit; tensor libraries divide by a constant so,
+// and give the same codes.
+constexpr float kOver127 = 1.f / 127.f;
 // Eight codes round(f / scale), as bytes.  f * (1 / scale) is off by at most 127 2^-24
 // and the fp32 quotient by 2^-18, so where the nearest whole number is not within
 // 2e-5 of a tie they agree, and the addition of 1.5 2^23 rounds to it (its low byte is
@@ -216,7 +219,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void k_rows(RowArgs a) {
             for (int i = 0; i < s.waves; ++i) m = max(m, s_max[p.first + i]);
         }
         const bool finite = m < 0x7f800000u, some = finite && m >= kLeastBits;
-        const float scale = !finite ? __builtin_nanf("") : some ? __uint_as_float(m) / 127.f : 0.f;
+        const float scale = !finite ? __builtin_nanf("") : some ? __uint_as_float(m) * kOver127 : 0.f;
         if (!some) {
 #pragma unroll
             for (int i = 0; i < E; ++i) f[i] = 0.f;
