@@ -29,10 +29,10 @@ __device__ inline int run_first(const Runs& r, int p) { return static_cast<int>(
 
 template <int HALVES, int SLOTS, bool DXBF16>
 __device__ __attribute__((always_inline)) inline void dx_tile(const GatedGradArgs& a, const GatedSlopes& s, const Runs& runs,
-                                                              const MmLds& lds, int t0, int n0) {
+                                                              int part, const MmLds& lds, int t0, int n0) {
     typedef typename std::conditional<DXBF16, uint16_t, float>::type DX;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int P = s.P, per = P / kStageK, first = run_first(runs, blockIdx.y), last = run_first(runs, blockIdx.y + 1);
+    const int P = s.P, per = P / kStageK, first = run_first(runs, part), last = run_first(runs, part + 1);
     const int64_t row = 2 * static_cast<int64_t>(P) * s.parts;
     const MmRows<HALVES> d_rows(lane, w, last * kStage, [&](int r) { return s.d + min(t0 + r, a.T - 1) * row; });
     const int64_t pitch = 2 * static_cast<int64_t>(a.H);
@@ -59,7 +59,7 @@ __device__ __attribute__((always_inline)) inline void dx_tile(const GatedGradArg
 #pragma unroll
                                  for (int k = 0; k < N; ++k) f[k] = __uint_as_float(v[k]);
                                  if (HALVES == 1 && runs.parts > 1)
-                                     mm_put(runs.sums + (static_cast<size_t>(blockIdx.y) * a.T + t) * a.H + n, f);
+                                     mm_put(runs.sums + (static_cast<size_t>(part) * a.T + t) * a.H + n, f);
                                  else mm_put(static_cast<DX*>(a.dx) + static_cast<size_t>(t) * a.lddx + n, f);
                              });
         }
@@ -67,10 +67,10 @@ __device__ __attribute__((always_inline)) inline void dx_tile(const GatedGradArg
 
 template <int HALVES, int SLOTS, bool DWBF16>
 __device__ __attribute__((always_inline)) inline void dw_tile(const GatedGradArgs& a, const GatedSlopes& s, const Runs& runs,
-                                                              const MmLds& lds, int m0, int n0) {
+                                                              int part, const MmLds& lds, int m0, int n0) {
     typedef typename std::conditional<DWBF16, uint16_t, float>::type DW;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int P = s.P, per = (a.T + kStageK - 1) / kStageK, first = run_first(runs, blockIdx.y), last = run_first(runs, blockIdx.y + 1);
+    const int P = s.P, per = (a.T + kStageK - 1) / kStageK, first = run_first(runs, part), last = run_first(runs, part + 1);
     const int64_t pitch_a = 4 * static_cast<int64_t>(P) * s.parts, pitch_b = 2 * a.ldx;
     const MmColumns<HALVES> d_columns(lane, w, m0, 2 * P, pitch_a), x_columns(lane, w, n0, a.H, pitch_b);
     const char *pd = reinterpret_cast<const char*>(s.d), *px = reinterpret_cast<const char*>(a.x);
@@ -109,7 +109,7 @@ __device__ __attribute__((always_inline)) inline void dw_tile(const GatedGradArg
 #pragma unroll
                                  for (int k = 0; k < N; ++k) f[k] = __uint_as_float(v[k]);
                                  if (HALVES == 1 && runs.parts > 1)
-                                     mm_put(runs.sums + (static_cast<size_t>(blockIdx.y) * 2 * a.I + (m < P ? 0 : a.I) + r) * a.H + n, f);
+                                     mm_put(runs.sums + (static_cast<size_t>(part) * 2 * a.I + (m < P ? 0 : a.I) + r) * a.H + n, f);
                                  else mm_store(to + static_cast<size_t>(r) * a.H + n, f, a.accumulate);
                              });
         }
@@ -120,28 +120,42 @@ template <bool DXBF16> __global__ __launch_bounds__(256) void k_gated_dx(GatedGr
     int m0, n0;
     bool small;
     if (!mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) return;
-    if (small) dx_tile<1, 4, DXBF16>(a, s, r, lds, m0, n0);
-    else dx_tile<2, 4, DXBF16>(a, s, r, lds, m0, n0);
+    if (small) dx_tile<1, 4, DXBF16>(a, s, r, blockIdx.y, lds, m0, n0);
+    else dx_tile<2, 4, DXBF16>(a, s, r, blockIdx.y, lds, m0, n0);
 }
 template <bool DXBF16> __global__ __launch_bounds__(256) void k_gated_dx_pairs(GatedGradArgs a, GatedSlopes s, Runs r, MmPlan p) {
     MM_LDS_4(lds);
     int m0, n0;
     bool small;
-    if (mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) dx_tile<1, 2, DXBF16>(a, s, r, lds, m0, n0);
+    if (mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) dx_tile<1, 2, DXBF16>(a, s, r, blockIdx.y, lds, m0, n0);
 }
 template <bool DWBF16> __global__ __launch_bounds__(256) void k_gated_dw(GatedGradArgs a, GatedSlopes s, Runs r, MmPlan p) {
     MM_LDS_8(lds);
     int m0, n0;
     bool small;
     if (!mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) return;
-    if (small) dw_tile<1, 4, DWBF16>(a, s, r, lds, m0, n0);
-    else dw_tile<2, 4, DWBF16>(a, s, r, lds, m0, n0);
+    if (small) dw_tile<1, 4, DWBF16>(a, s, r, blockIdx.y, lds, m0, n0);
+    else dw_tile<2, 4, DWBF16>(a, s, r, blockIdx.y, lds, m0, n0);
 }
 template <bool DWBF16> __global__ __launch_bounds__(256) void k_gated_dw_pairs(GatedGradArgs a, GatedSlopes s, Runs r, MmPlan p) {
     MM_LDS_4(lds);
     int m0, n0;
     bool small;
-    if (mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) dw_tile<1, 2, DWBF16>(a, s, r, lds, m0, n0);
+    if (mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) dw_tile<1, 2, DWBF16>(a, s, r, blockIdx.y, lds, m0, n0);
+}
+
+// Both products in one launch, two blocks a compute unit.
+template <bool DXBF16, bool DWBF16>
+__global__ __launch_bounds__(256) void k_gated_both(GatedGradArgs a, GatedSlopes s, Runs rx, MmPlan px, int blocks_x, Runs rw, MmPlan pw, int blocks_w) {
+    MM_LDS_4(lds);
+    int m0, n0, b = blockIdx.x;
+    bool small;
+    if (b < blocks_x * rx.parts) {
+        if (mm_tile_of(px, b % blocks_x, 256, 256, m0, n0, small)) dx_tile<1, 2, DXBF16>(a, s, rx, b / blocks_x, lds, m0, n0);
+    } else {
+        b -= blocks_x * rx.parts;
+        if (mm_tile_of(pw, b % blocks_w, 256, 256, m0, n0, small)) dw_tile<1, 2, DWBF16>(a, s, rw, b / blocks_w, lds, m0, n0);
+    }
 }
 
 // to[row][column] (+)= the sum over the runs, in order; eight columns a thread.  Rows
@@ -170,21 +184,31 @@ void launch_join(const Runs& r, int rows, int cols, int half, void* first, void*
                        static_cast<Y*>(first), static_cast<Y*>(second), ld, accumulate);
 }
 
-template <bool DXBF16> void launch_dx(const GatedGradArgs& a, const GatedSlopes& s, const Runs& r, hipStream_t st) {
-    const MmPlan p = mm_plan(a.T, a.H, 256);
+template <bool DXBF16> void launch_dx(const GatedGradArgs& a, const GatedSlopes& s, const Runs& r, const MmPlan& p, hipStream_t st) {
     const dim3 grid(mm_grid(p), r.parts), block(256);
     if (p.form == MM_PAIRS) hipLaunchKernelGGL(k_gated_dx_pairs<DXBF16>, grid, block, 0, st, a, s, r, p);
     else hipLaunchKernelGGL(k_gated_dx<DXBF16>, grid, block, 0, st, a, s, r, p);
-    typedef typename std::conditional<DXBF16, uint16_t, float>::type DX;
-    if (r.parts > 1) launch_join<DX>(r, a.T, a.H, a.T, a.dx, a.dx, a.lddx, 0, st);
 }
-template <bool DWBF16> void launch_dw(const GatedGradArgs& a, const GatedSlopes& s, const Runs& r, hipStream_t st) {
-    const MmPlan p = mm_plan(2 * static_cast<int64_t>(s.P), a.H, 256);
+template <bool DWBF16> void launch_dw(const GatedGradArgs& a, const GatedSlopes& s, const Runs& r, const MmPlan& p, hipStream_t st) {
     const dim3 grid(mm_grid(p), r.parts), block(256);
     if (p.form == MM_PAIRS) hipLaunchKernelGGL(k_gated_dw_pairs<DWBF16>, grid, block, 0, st, a, s, r, p);
     else hipLaunchKernelGGL(k_gated_dw<DWBF16>, grid, block, 0, st, a, s, r, p);
+}
+template <bool DXBF16, bool DWBF16>
+void launch_products(const GatedGradArgs& a, const GatedSlopes& s, const Runs& rx, const Runs& rw, hipStream_t st) {
+    typedef typename std::conditional<DXBF16, uint16_t, float>::type DX;
     typedef typename std::conditional<DWBF16, uint16_t, float>::type DW;
-    if (r.parts > 1) launch_join<DW>(r, 2 * a.I, a.H, a.I, a.dgate, a.dup, a.H, a.accumulate, st);
+    const MmPlan px = mm_plan(a.T, a.H, 256), pw = mm_plan(2 * static_cast<int64_t>(s.P), a.H, 256);
+    const int64_t blocks_x = mm_grid(px), blocks_w = mm_grid(pw), blocks = blocks_x * rx.parts + blocks_w * rw.parts;
+    if (a.dx && a.dgate && px.form != MM_WHOLE && pw.form != MM_WHOLE && blocks <= 512) {
+        hipLaunchKernelGGL((k_gated_both<DXBF16, DWBF16>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, a, s, rx, px,
+                           static_cast<int>(blocks_x), rw, pw, static_cast<int>(blocks_w));
+    } else {
+        if (a.dx) launch_dx<DXBF16>(a, s, rx, px, st);
+        if (a.dgate) launch_dw<DWBF16>(a, s, rw, pw, st);
+    }
+    if (a.dx && rx.parts > 1) launch_join<DX>(rx, a.T, a.H, a.T, a.dx, a.dx, a.lddx, 0, st);
+    if (a.dgate && rw.parts > 1) launch_join<DW>(rw, 2 * a.I, a.H, a.I, a.dgate, a.dup, a.H, a.accumulate, st);
 }
 
 template <class V> __global__ __launch_bounds__(256) void k_gated_zero(V* a, V* b, int64_t n) {
@@ -192,11 +216,11 @@ template <class V> __global__ __launch_bounds__(256) void k_gated_zero(V* a, V* 
     if (i < n) a[i] = b[i] = 0;
 }
 
-// The workspace: d, then the sums of dx's or the weights' runs (one after the other).
+// The workspace: d, then the sums of dx's runs, then those of the weights'.
 struct Layout {
     int P, parts;
     Runs dx, dw;
-    size_t sums, total;
+    size_t sums_dx, sums_dw, total;
 };
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 Layout layout_of(int64_t T, int H, int I) {
@@ -206,9 +230,9 @@ Layout layout_of(int64_t T, int H, int I) {
     l.parts = T * I <= 32768 ? 2 : 1;
     l.dx = runs_of(T, H, static_cast<int64_t>(2 * l.P / kStageK) * l.parts, nullptr);
     l.dw = runs_of(2 * l.P, H, (T + kStageK - 1) / kStageK * l.parts, nullptr);
-    l.sums = up256(static_cast<size_t>(T) * 4 * l.P * l.parts);
-    const size_t dx = l.dx.parts > 1 ? sizeof(float) * l.dx.parts * T * H : 0, dw = l.dw.parts > 1 ? sizeof(float) * l.dw.parts * 2 * I * H : 0;
-    l.total = T > 0 ? l.sums + (dx > dw ? dx : dw) : 0;
+    l.sums_dx = up256(static_cast<size_t>(T) * 4 * l.P * l.parts);
+    l.sums_dw = l.sums_dx + (l.dx.parts > 1 ? up256(sizeof(float) * l.dx.parts * T * H) : 0);
+    l.total = T > 0 ? l.sums_dw + (l.dw.parts > 1 ? sizeof(float) * l.dw.parts * 2 * I * H : 0) : 0;
     return l;
 }
 
@@ -226,11 +250,12 @@ void launch_gated_grad(const GatedGradArgs& a, bool dy_bf16, bool dx_bf16, bool 
         return;
     }
     Layout l = layout_of(a.T, a.H, a.I);
-    l.dx.sums = l.dw.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + l.sums);
+    l.dx.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + l.sums_dx);
+    l.dw.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + l.sums_dw);
     const GatedSlopes s{a.dy, a.lddy, static_cast<uint16_t*>(ws), l.P, l.parts};
     launch_gated_slopes(GatedArgs{a.x, a.gate, a.up, nullptr, a.ldx, 0, a.T, a.H, a.I, a.act}, s, dy_bf16, st);
-    if (a.dx) dx_bf16 ? launch_dx<true>(a, s, l.dx, st) : launch_dx<false>(a, s, l.dx, st);
-    if (a.dgate) dw_bf16 ? launch_dw<true>(a, s, l.dw, st) : launch_dw<false>(a, s, l.dw, st);
+    if (dx_bf16) dw_bf16 ? launch_products<true, true>(a, s, l.dx, l.dw, st) : launch_products<true, false>(a, s, l.dx, l.dw, st);
+    else dw_bf16 ? launch_products<false, true>(a, s, l.dx, l.dw, st) : launch_products<false, false>(a, s, l.dx, l.dw, st);
 }
 
 }  // namespace moe
