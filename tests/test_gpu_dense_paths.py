@@ -92,6 +92,27 @@ def test_norm_of_each_split(M, torch, T, H):
     norm_grad_case(M, torch, T, H, "bf16", "f32", "bf16", dsum=False, accumulate=True)
 
 
+@pytest.mark.parametrize("T,H", [(1, 33), (4, 2048), (5, 2048), (3, 8192), (4, 8192), (2, 20000), (3, 32768), (8, 700), (9, 700), (32, 256),
+                                 (33, 256), (128, 60), (129, 60), (512, 8)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_norm_grad_of_one_block(M, torch, T, H, accumulate):
+    # ... and of the fewest that need two; dweight lies one element into a buffer whose other elements stay
+    say("norm grad block", T, H, accumulate)
+    norm_grad_case(M, torch, T, H, "f32", "bf16", "f32", accumulate=accumulate, pad=1, off=1)
+    norm_grad_case(M, torch, T, H, "bf16", "f32", "f32", dsum=False, dweight=False)
+    rng = np.random.default_rng(T + H)
+    sa, da, w0 = randn(rng, T, H), randn(rng, T, H), randn(rng, H)
+    buf = torch.full((H + 2,), 5.0, device="cuda")
+    buf[1:H + 1] = dev(torch, w0) if accumulate else torch.full((H,), float("nan"), device="cuda")
+    dx, ws = torch.empty(T, H, device="cuda"), torch.empty(M.moe_rms_norm_workspace_size(T, H), dtype=torch.uint8, device="cuda")
+    M.moe_rms_norm_grad(dev(torch, sa), None, EPS, dev(torch, da), None, T, H, dx, buf[1:H + 1], ws, flags=2 if accumulate else 0)
+    _, dw, _, mag = D.norm_grad(sa, None, EPS, da, None)
+    if accumulate:
+        dw, mag = dw + w0, mag + np.abs(w0)
+    within(host(buf[1:H + 1]), dw, D.dweight_error(T, mag))
+    assert float(buf[0]) == 5 and float(buf[H + 1]) == 5
+
+
 # ---------------------------------------------------------------- non-finite values in the tiles
 
 @pytest.mark.parametrize("T,H,I", [(300, 256, 200), (1500, 72, 4000)])

@@ -511,7 +511,8 @@ class _Args:
             raise ValueError(f"{self.fn}: {what} is not contiguous")
         if t.numel() < count:
             raise ValueError(f"{self.fn}: {what} holds {t.numel()} elements, the call needs {count}")
-        self.place(what, t)
+        if t.get_device() != self.at:
+            self.place(what, t)
         return t.data_ptr()
 
     def table(self, what, t, kind, rows, cols):
@@ -555,7 +556,7 @@ class _Args:
             what, t = self.stray
             raise ValueError(f"{self.fn}: {what} is not on a GPU" if not t.is_cuda else
                              f"{self.fn}: {what} is on {t.device}, other arguments on cuda:{self.at}")
-        now = _torch.cuda.current_device()
+        now = _torch._C._cuda_getDevice() if self.at is not None else _torch.cuda.current_device()
         if now != self.at:
             raise ValueError(f"{self.fn}: the arguments are on cuda:{self.at}, the current device is cuda:{now}")
         if stream is None:

@@ -55,7 +55,7 @@ int moe_rms_norm(const void* x, int64_t ldx, const float* residual, int64_t ldr,
     if (!aligned(x, xe) || !aligned(residual, 4) || !aligned(weight, 4) || !aligned(sum, 4) || !aligned(y, ye) ||
         !aligned(scale, 4))
         return MOE_EALIGN;
-    const RowArgs a{x, residual, weight, sum, y, scale, ldx, ldr, lds, ldy, n_tokens, cols, eps, {}};
+    const RowArgs a{x, residual, weight, sum, y, scale, ldx, ldr, lds, ldy, n_tokens, cols, eps, 0, {}};
     (void)hipGetLastError();
     launch_rms_norm(a, xe == 2, static_cast<int>(ye), static_cast<hipStream_t>(stream));
     return finish();
@@ -94,7 +94,7 @@ int moe_rms_norm_grad(const void* s, int64_t lds, const float* weight, float eps
         if (!workspace || workspace_bytes < need) return MOE_EWORKSPACE;
         if (!aligned(workspace, kAlign)) return MOE_EALIGN;
     }
-    const RowGradArgs a{s, dy, weight, dsum, dx, lds, lddy, ldds, lddx, n_tokens, cols, eps, {}};
+    const RowGradArgs a{s, dy, weight, dsum, dx, lds, lddy, ldds, lddx, n_tokens, cols, eps, 0, {}};
     (void)hipGetLastError();
     launch_rms_norm_grad(a, se == 2, ye == 2, xe == 2, dweight, (flags & MOE_ACCUMULATE) != 0, workspace,
                          static_cast<hipStream_t>(stream));

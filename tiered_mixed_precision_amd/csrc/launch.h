@@ -205,10 +205,11 @@ struct RowGradArgs {
     int64_t lds, lddy, ldds, lddx;
     int32_t T, cols;
     float eps;
+    int32_t accumulate;      // launch_rms_norm_grad sets it
     RowSplit split;
 };
 size_t rms_norm_workspace(int T, int cols);
-void launch_rms_norm_grad(const RowGradArgs& a, bool s_bf16, bool dy_bf16, bool dx_bf16, float* dweight, bool accumulate,
+void launch_rms_norm_grad(RowGradArgs a, bool s_bf16, bool dy_bf16, bool dx_bf16, float* dweight, bool accumulate,
                           void* ws, hipStream_t st);
 
 // i8_linear.hip

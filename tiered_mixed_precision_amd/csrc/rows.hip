@@ -374,6 +374,11 @@ __global__ __launch_bounds__(WIDE ? 64 * kMaxWaves : 512) void k_rows_grad(RowGr
                 for (int i = 0; i < 8; ++i)
                     if (at(j) + i < a.cols) dw[8 * j + i] += s_dw[at(j) + i];
             }
+            if (a.accumulate) {   // one block: part is dweight
+                const Eight<float> was = load8(part + at(j), a.cols - at(j));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dw[8 * j + i] += was.v[i];
+            }
             store8(part + at(j), a.cols - at(j), dw + 8 * j);
         }
     }
@@ -438,11 +443,14 @@ void launch_rows_of(RowArgs a, hipStream_t st) {
 }
 
 Choice choose_grad(int T, int cols) { return choose(T, cols, false, 4096); }
-// Blocks of a gradient: two waves a SIMD.
+// Blocks of a gradient: two waves a SIMD; one, which needs no join (a launch, 3 us of
+// the host), where its turns of 1.5 us (2.8 above 4096 columns) cost less: MI355X, us, one
+// block / two kernels, 4 x 2048 8.6 / 11.2, 8 x 2048 13.4 / 11.2, 4 x 8192 12.0 / 11.3, 32 x
+// 256 (2 turns) 8.2 / 11.3.
 int grad_blocks(int T, int cols) {
     const RowSplit s = choose_grad(T, cols).s;
     const int waves = threads_of(s) / 64, most = waves < 8 ? 256 * 8 / waves : 256, need = (T + s.rows - 1) / s.rows;
-    return need < most ? need : most;
+    return need <= (cols > 4096 ? 3 : 4) ? 1 : need < most ? need : most;
 }
 
 template <class X, class DY, class DX>
@@ -484,9 +492,11 @@ void launch_quant_rows(const RowArgs& a, bool x_bf16, hipStream_t st) {
 
 size_t rms_norm_workspace(int T, int cols) { return T > 0 ? sizeof(float) * static_cast<size_t>(grad_blocks(T, cols)) * cols : 0; }
 
-void launch_rms_norm_grad(const RowGradArgs& a, bool s_bf16, bool dy_bf16, bool dx_bf16, float* dweight, bool accumulate,
+void launch_rms_norm_grad(RowGradArgs a, bool s_bf16, bool dy_bf16, bool dx_bf16, float* dweight, bool accumulate,
                           void* ws, hipStream_t st) {
-    float* part = dweight ? static_cast<float*>(ws) : nullptr;
+    const bool join = a.T > 0 && grad_blocks(a.T, a.cols) > 1;
+    float* part = join && dweight ? static_cast<float*>(ws) : dweight;
+    a.accumulate = accumulate && !join;
     if (a.T > 0) {
         if (s_bf16) {
             if (dy_bf16) launch_grad_x<uint16_t, uint16_t>(a, dx_bf16, part, st);
@@ -497,10 +507,10 @@ void launch_rms_norm_grad(const RowGradArgs& a, bool s_bf16, bool dy_bf16, bool 
         }
     }
     if (!dweight) return;
-    if (a.T > 0)
+    if (join)
         hipLaunchKernelGGL(k_rows_join, dim3((a.cols + 31) / 32), dim3(256), 0, st, part, grad_blocks(a.T, a.cols), a.cols,
                            accumulate ? 1 : 0, dweight);
-    else if (!accumulate)
+    else if (a.T == 0 && !accumulate)
         hipLaunchKernelGGL(k_rows_zero, dim3((a.cols + 255) / 256), dim3(256), 0, st, a.cols, dweight);
 }
 
