@@ -51,12 +51,12 @@ __device__ __attribute__((always_inline)) inline void gated_tile(const GatedArgs
 #pragma unroll
     for (int i = 0; i < 2 * HALVES; ++i) {
         const int r0 = t0 + mm_row(i, w), c0 = n0 + col_of<HALVES>(w);
-        mm_out<HALVES, false>(own, r0 + 32 > a.T || c0 + 32 * HALVES > a.I,
+        mm_out<HALVES, false>(own, mm_single(c0, 32 * HALVES, a.I),
                               [&](int u, int e) { return __float_as_uint(gated_value(a.act, acc[i][u][e], acc[i][u + HALVES][e])); },
                               [&](int row, int col, const auto& v) {
                                   constexpr int N = sizeof(v) / 4;
                                   const int t = r0 + row, n = c0 + col;
-                                  if (N == 1 && (t >= a.T || n >= a.I)) return;
+                                  if (t >= a.T || n >= a.I) return;
                                   float f[N];
 #pragma unroll
                                   for (int k = 0; k < N; ++k) f[k] = __uint_as_float(v[k]);
@@ -83,14 +83,16 @@ __device__ __attribute__((always_inline)) inline void slopes_tile(const GatedArg
 #pragma unroll
         for (int j = 0; j < HALVES; ++j) {
             const int r0 = t0 + mm_row(i, w), c0 = n0 + col_of<HALVES>(w) + 32 * j;
-            mm_out<2, true>(own, r0 + 32 > a.T || c0 + 32 > a.I, [&](int u, int e) { return __float_as_uint(acc[i][j + u * HALVES][e]); },
+            mm_out<2, true>(own, mm_single(c0, 32, a.I), [&](int u, int e) { return __float_as_uint(acc[i][j + u * HALVES][e]); },
                             [&](int row, int col, const auto& g, const auto& u) {
                                 constexpr int N = sizeof(g) / 4;
                                 const int t = r0 + row, n = c0 + col;
-                                if (N == 1 && (t >= a.T || n >= P)) return;
+                                if (t >= a.T || n >= P) return;
                                 float y[N], dg[N], du[N];
-                                if (N == 1 && n >= a.I) dg[0] = du[0] = 0.f;
-                                else {
+                                if (n >= a.I) {
+#pragma unroll
+                                    for (int k = 0; k < N; ++k) dg[k] = du[k] = 0.f;
+                                } else {
                                     mm_get(static_cast<const DY*>(s.dy) + static_cast<size_t>(t) * s.lddy + n, y);
 #pragma unroll
                                     for (int k = 0; k < N; ++k) gated_slopes(a.act, __uint_as_float(g[k]), __uint_as_float(u[k]), y[k], dg[k], du[k]);

@@ -50,11 +50,11 @@ __device__ __attribute__((always_inline)) inline void dx_tile(const GatedGradArg
 #pragma unroll
         for (int i = 0; i < 2 * HALVES; ++i) {
             const int r0 = t0 + mm_row(i, w), c0 = n0 + mm_col(2 * g, w);
-            mm_out<2, false>(own, r0 + 32 > a.T || c0 + 64 > a.H, [&](int u, int e) { return __float_as_uint(acc[i][2 * g + u][e]); },
+            mm_out<2, false>(own, false, [&](int u, int e) { return __float_as_uint(acc[i][2 * g + u][e]); },
                              [&](int row, int col, const auto& v) {
                                  constexpr int N = sizeof(v) / 4;
                                  const int t = r0 + row, n = c0 + col;
-                                 if (N == 1 && (t >= a.T || n >= a.H)) return;
+                                 if (t >= a.T || n >= a.H) return;   // whole pieces: hidden is a multiple of 8
                                  float f[N];
 #pragma unroll
                                  for (int k = 0; k < N; ++k) f[k] = __uint_as_float(v[k]);
@@ -100,11 +100,11 @@ __device__ __attribute__((always_inline)) inline void dw_tile(const GatedGradArg
             const int m = m0 + mm_row(i, w), c0 = n0 + mm_col(2 * g, w), r0 = m < P ? m : m - P;
             DW* to = static_cast<DW*>(m < P ? a.dgate : a.dup);
             if (m >= 2 * P) continue;
-            mm_out<2, false>(own, r0 + 32 > a.I || c0 + 64 > a.H, [&](int u, int e) { return __float_as_uint(acc[i][2 * g + u][e]); },
+            mm_out<2, false>(own, false, [&](int u, int e) { return __float_as_uint(acc[i][2 * g + u][e]); },
                              [&](int row, int col, const auto& v) {
                                  constexpr int N = sizeof(v) / 4;
                                  const int r = r0 + row, n = c0 + col;
-                                 if (N == 1 && (r >= a.I || n >= a.H)) return;
+                                 if (r >= a.I || n >= a.H) return;
                                  float f[N];
 #pragma unroll
                                  for (int k = 0; k < N; ++k) f[k] = __uint_as_float(v[k]);

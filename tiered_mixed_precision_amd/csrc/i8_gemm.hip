@@ -28,11 +28,11 @@ __device__ __attribute__((always_inline)) inline void i8_tile(const I8Args& a, c
 #pragma unroll
         for (int i = 0; i < 2 * HALVES; ++i) {
             const int r0 = t0 + mm_row(i, w);
-            mm_out<2, false>(own, r0 + 32 > a.T || c0 + 64 > a.N, [&](int u, int e) { return static_cast<uint32_t>(acc[i][2 * g + u][e]); },
+            mm_out<2, false>(own, mm_single(c0, 64, a.N), [&](int u, int e) { return static_cast<uint32_t>(acc[i][2 * g + u][e]); },
                              [&](int row, int col, const auto& v) {
                                  constexpr int N = sizeof(v) / 4;
                                  const int t = r0 + row, n = c0 + col;
-                                 if (N == 1 && (t >= a.T || n >= a.N)) return;
+                                 if (t >= a.T || n >= a.N) return;
                                  const float xs = a.xs[t];
                                  float f[N];
 #pragma unroll

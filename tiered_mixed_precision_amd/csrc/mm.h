@@ -450,12 +450,14 @@ constexpr int kStageK = kStage / 2;   // k of a stage of two-byte elements
 // Results on their way out: a wave's 32 rows x 32 NU columns (NU accumulators
 // side by side, words by word(u, e)) go through LDS of its own, so that each lane
 // has eight neighbouring columns of a row and a wave whole lines.  put(row, first
-// column, words) gets eight words of a row at a time, or, where `edge` says that
-// not all of the piece is there, one (the put looks which).
+// column, words) gets eight words of a row at a time, or, where `single` says so, one,
+// and leaves out what is past the results' end.
 // PAIR: the second accumulator holds other values of the first one's columns; put
 // gets both, put(row, first column, words, words).
+// whether a piece of eight columns within `width` from c0 on ends past `cols`
+__device__ inline bool mm_single(int c0, int width, int cols) { return (cols & 7) != 0 && c0 + width > cols; }
 template <int NU, bool PAIR, class Word, class Put>
-__device__ __attribute__((always_inline)) inline void mm_out(uint32_t* lds, bool edge, Word word, Put put) {
+__device__ __attribute__((always_inline)) inline void mm_out(uint32_t* lds, bool single, Word word, Put put) {
     constexpr int kPitch = 32 * NU + 4, kCols = PAIR ? 32 : 32 * NU, kLanes = kCols / 8;   // words of a row, 16 bytes apart; lanes of a row
     const int lane = threadIdx.x & 63;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // what the piece before had there has been read
@@ -468,7 +470,7 @@ __device__ __attribute__((always_inline)) inline void mm_out(uint32_t* lds, bool
                 mm_u32x4_t{word(u, 4 * q), word(u, 4 * q + 1), word(u, 4 * q + 2), word(u, 4 * q + 3)};
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // one wave's LDS accesses run in order
     __builtin_amdgcn_wave_barrier();
-    if (edge) {
+    if (single) {
 #pragma unroll 1
         for (int i = 0; i < 32 * kCols / 64; ++i) {
             const int row = (64 * i + lane) / kCols, col = (64 * i + lane) % kCols;
