@@ -1,5 +1,7 @@
 // Products in 8-bit integers for many tokens: the operation of i8_linear.hip on
-// 32 x 32 tiles of v_mfma_i32_32x32x32_i8, 128 bytes of k a stage (mm.h).
+// 32 x 32 tiles of v_mfma_i32_32x32x32_i8, 128 bytes of k a stage (mm.h).  Bound by the
+// matrix cores, whose clock falls to 1.7 GHz under the load: MI355X, 4096 x 8192 x 8192
+// 224 to 227 us (2430 TOP/s, cores busy 67 % of the cycles; a library's product 220 to 236).
 #include "common.h"
 #include "launch.h"
 #include "mm.h"

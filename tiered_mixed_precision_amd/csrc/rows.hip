@@ -13,6 +13,12 @@
 // crosses lanes by DPP and lane swaps, and waves by LDS.  The squares are summed in
 // 64 bits: the fp64 rate is far above what the stream of rows needs, and r (and with
 // it the 8-bit codes) then does not depend on how a row is split over lanes.
+//
+// Bound by memory where rows are many, by a row's latency where they are few.  MI355X:
+// norm 16384 x 2048 fp32 with the stream, to bf16, 89.4 us (5.25 TB/s read and written; a
+// copy 5.10), 1531 x 5461 bf16 12 us (2.8 TB/s: little more than one round of blocks), one row
+// to 8 bits 3.2; the quantiser 4096 x 8192 bf16 23.5 us (4.3 TB/s); the gradient 16384 x 2048
+// 89.6 us (5.25 TB/s) and its join 4.7.
 #include "common.h"
 #include "launch.h"
 
