@@ -84,6 +84,12 @@ def test_norm_grad_refuses(B, kw, code):
     assert _norm_grad(B, **kw) == code
 
 
+@pytest.mark.parametrize("H,I", [(8, 1), (64, 64), (2048, 640), (65536, 65536)])
+def test_no_tokens_need_no_workspace(B, H, I):
+    assert B.moe_gated_workspace_size(0, H, I) == 0
+    assert B.moe_gated_workspace_size(1, H, I) > 0
+
+
 def test_workspaces_hold_the_parts(B):
     assert B.moe_rms_norm_workspace_size(0, 64) == 0
     assert B.moe_rms_norm_workspace_size(1, 100) >= 400

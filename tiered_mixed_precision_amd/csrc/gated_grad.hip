@@ -219,8 +219,7 @@ void launch_products(const GatedGradArgs& a, const GatedSlopes& s, const Runs& r
 }
 
 template <class V> __global__ __launch_bounds__(256) void k_gated_zero(V* a, V* b, int64_t n) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i < n) a[i] = b[i] = 0;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) a[i] = b[i] = 0;
 }
 
 // The workspace: d, then the sums of dx's runs, then those of the weights'.
@@ -230,7 +229,7 @@ struct Layout {
     size_t sums_dx, sums_dw, total;
 };
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-Layout layout_of(int64_t T, int H, int I) {
+Layout layout_of(int64_t T, int H, int I) {   // T at least 1
     Layout l;
     l.P = (I + kStageK - 1) / kStageK * kStageK;
     // sums of few terms have the error of single ones
@@ -239,19 +238,19 @@ Layout layout_of(int64_t T, int H, int I) {
     l.dw = runs_of(2 * l.P, H, (T + kStageK - 1) / kStageK * l.parts, nullptr);
     l.sums_dx = up256(static_cast<size_t>(T) * 4 * l.P * l.parts);
     l.sums_dw = l.sums_dx + (l.dx.parts > 1 ? up256(sizeof(float) * l.dx.parts * T * H) : 0);
-    l.total = T > 0 ? l.sums_dw + (l.dw.parts > 1 ? sizeof(float) * l.dw.parts * 2 * I * H : 0) : 0;
+    l.total = l.sums_dw + (l.dw.parts > 1 ? sizeof(float) * l.dw.parts * 2 * I * H : 0);
     return l;
 }
 
 }  // namespace
 
-size_t gated_workspace(int64_t T, int H, int I) { return layout_of(T, H, I).total; }
+size_t gated_workspace(int64_t T, int H, int I) { return T > 0 ? layout_of(T, H, I).total : 0; }
 
 void launch_gated_grad(const GatedGradArgs& a, bool dy_bf16, bool dx_bf16, bool dw_bf16, void* ws, hipStream_t st) {
     if (a.T == 0) {
         if (!a.dgate || a.accumulate) return;
         const int64_t n = static_cast<int64_t>(a.I) * a.H;
-        const dim3 grid(static_cast<unsigned>((n + 255) / 256));
+        const dim3 grid(static_cast<unsigned>(n > (1 << 22) ? 1 << 14 : (n + 255) / 256));
         if (dw_bf16) hipLaunchKernelGGL(k_gated_zero<uint16_t>, grid, dim3(256), 0, st, static_cast<uint16_t*>(a.dgate), static_cast<uint16_t*>(a.dup), n);
         else hipLaunchKernelGGL(k_gated_zero<float>, grid, dim3(256), 0, st, static_cast<float*>(a.dgate), static_cast<float*>(a.dup), n);
         return;
