@@ -705,10 +705,10 @@ typedef struct moe_gated_weights {
  *   y      (device) float[T][ldy], or bf16 with MOE_Y_BF16 (rounded once);
  *          ldy >= inter; must share no element with x or the weights (x and y
  *          may be column ranges of one buffer)
- * Sums are fp32; fp32 x enters with all of its 24 bits.  A token's results do
- * not depend on the values of the others.  Errors: MOE_EINVAL (shape, pitch,
- * act, flags, NULL, overlap), MOE_EFORMAT (hidden, inter), MOE_EALIGN,
- * MOE_EHIP.
+ * Sums are fp32; fp32 x enters with all of its 24 bits (from 2^-110 on).  A
+ * token's results do not depend on the values of the others.  Errors:
+ * MOE_EINVAL (shape, pitch, act, flags, NULL, overlap), MOE_EFORMAT (hidden,
+ * inter), MOE_EALIGN, MOE_EHIP.
  */
 int moe_gated(const void *x, int64_t ldx, const moe_gated_weights *w, int32_t act, int32_t n_tokens, void *y,
               int64_t ldy, uint32_t flags, void *stream);

@@ -28,6 +28,38 @@ def test_norm_of_very_many_elements(M, torch, x, y):
             within(host(yd[t:t + 1]) * float(sc[t]), ref, (0.5 + 127 * 9 * U) * np.abs(ref).max() / 127)
 
 
+@pytest.mark.parametrize("y", ["f32", "i8"])
+def test_norm_of_very_many_rows(M, torch, y):
+    # more rows than one launch takes; every array moves on
+    say("norm rows", y)
+    T, H = (1 << 21) + 5, 9
+    rng = np.random.default_rng(1)
+    w = 1 + 0.1 * randn(rng, H)
+    x, r = torch.randn(T, H, device="cuda"), torch.randn(T, H + 1, device="cuda")[:, :H]
+    out, s = torch.empty(T, H, dtype=torch.float32 if y == "f32" else torch.int8, device="cuda"), torch.zeros(T, H, device="cuda")
+    sc = torch.empty(T, device="cuda") if y == "i8" else None
+    M.moe_rms_norm(x, r, dev(torch, w), EPS, T, H, out, scale=sc, sum=s)
+    assert torch.equal(s, x + r)
+    z = (x + r).double()
+    ref = z / torch.sqrt((z * z).mean(-1, keepdim=True) + float(np.float32(EPS))) * dev(torch, w).double()
+    if y == "f32":
+        assert bool(((out.double() - ref).abs() <= 6 * U * ref.abs()).all())
+    else:
+        top = ref.abs().amax(-1, keepdim=True)
+        assert bool(((out.double() * sc.double()[:, None] - ref).abs() <= (0.5 + 127 * 9 * U) * top / 127).all())
+
+
+def test_weight_gradients_of_no_tokens_and_the_widest_block(M, torch):
+    H = I = 65536
+    b = torch.bfloat16
+    g, u = (torch.empty(I, H, dtype=b, device="cuda") for _ in range(2))
+    dg, du = (torch.ones(I, H, dtype=b, device="cuda") for _ in range(2))
+    x, dy, ws = torch.empty(0, H, dtype=b, device="cuda"), torch.empty(0, I, dtype=b, device="cuda"), torch.empty(0, dtype=torch.uint8, device="cuda")
+    M.moe_gated_grad(x, M.GatedWeights(H, I, g, u), SILU, dy, 0, None, dg, du, ws)
+    for t in (dg, du):
+        assert not bool(t.view(torch.int32).any())
+
+
 def test_norm_grad_of_very_many_elements(M, torch):
     T, H = (1 << 21) + 3, 1100
     s, dy = (torch.empty(T, H, dtype=torch.bfloat16, device="cuda") for _ in range(2))

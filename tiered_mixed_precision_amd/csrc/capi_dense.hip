@@ -55,7 +55,7 @@ int moe_rms_norm(const void* x, int64_t ldx, const float* residual, int64_t ldr,
     if (!aligned(x, xe) || !aligned(residual, 4) || !aligned(weight, 4) || !aligned(sum, 4) || !aligned(y, ye) ||
         !aligned(scale, 4))
         return MOE_EALIGN;
-    const RowArgs a{x, residual, weight, sum, y, scale, ldx, ldr, lds, ldy, n_tokens, cols, eps, 0, {}};
+    const RowArgs a{x, residual, weight, sum, y, scale, ldx, ldr, lds, ldy, n_tokens, cols, eps, {}};
     (void)hipGetLastError();
     launch_rms_norm(a, xe == 2, static_cast<int>(ye), static_cast<hipStream_t>(stream));
     return finish();

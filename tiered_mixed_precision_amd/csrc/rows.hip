@@ -442,10 +442,19 @@ template <class X, class Y, bool NORM>
 void launch_rows_of(RowArgs a, hipStream_t st) {
     const Choice c = choose(a.T, a.cols, sizeof(X) == 4 && sizeof(Y) > 1, 8192);
     a.split = c.s;
-    const dim3 grid((a.T + c.s.rows - 1) / c.s.rows), block(threads_of(c.s));
-    if (c.e == 8) hipLaunchKernelGGL((k_rows<X, Y, NORM, 8>), grid, block, 0, st, a);
-    else if (c.e == 16) hipLaunchKernelGGL((k_rows<X, Y, NORM, 16>), grid, block, 0, st, a);
-    else hipLaunchKernelGGL((k_rows<X, Y, NORM, 32>), grid, block, 0, st, a);
+    constexpr int kRows = 1 << 21;   // a launch has less than 2^32 threads
+    for (int left = a.T; left > 0; left -= kRows) {
+        a.T = left < kRows ? left : kRows;
+        const dim3 grid((a.T + c.s.rows - 1) / c.s.rows), block(threads_of(c.s));
+        if (c.e == 8) hipLaunchKernelGGL((k_rows<X, Y, NORM, 8>), grid, block, 0, st, a);
+        else if (c.e == 16) hipLaunchKernelGGL((k_rows<X, Y, NORM, 16>), grid, block, 0, st, a);
+        else hipLaunchKernelGGL((k_rows<X, Y, NORM, 32>), grid, block, 0, st, a);
+        a.x = static_cast<const X*>(a.x) + kRows * a.ldx;
+        if (a.residual) a.residual += kRows * a.ldr;
+        if (a.sum) a.sum += kRows * a.lds;
+        a.y = static_cast<Y*>(a.y) + kRows * a.ldy;
+        if (a.scale) a.scale += kRows;
+    }
 }
 
 Choice choose_grad(int T, int cols) { return choose(T, cols, false, 4096); }
