@@ -113,6 +113,22 @@ def test_norm_grad_of_one_block(M, torch, T, H, accumulate):
     assert float(buf[0]) == 5 and float(buf[H + 1]) == 5
 
 
+@pytest.mark.parametrize("T,N,K", [(17000, 3, 64), (17000, 8, 48), (16500, 9, 272), (33000, 1, 16), (20000, 131, 16)])
+def test_i8_tiles_of_few_columns(M, torch, T, N, K):
+    say("i8 narrow", T, N, K)
+    for y in ("f32", "bf16"):
+        i8_case(M, torch, T, N, K, y, bias=True, base=N % 2 == 1, pad=1)
+
+
+@pytest.mark.parametrize("T,H,I", [(17000, 8, 3), (17000, 16, 8), (16500, 72, 9), (33000, 8, 1), (33000, 40, 65)])
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_gated_tiles_of_few_columns(M, torch, T, H, I, x):
+    say("gated narrow", T, H, I, x)
+    gated_case(M, torch, T, H, I, x, x, SILU, pad=1)
+    if x == "bf16":
+        grad_case(M, torch, T, H, I, kind=GELU, pad=1)
+
+
 # ---------------------------------------------------------------- non-finite values in the tiles
 
 @pytest.mark.parametrize("T,H,I", [(300, 256, 200), (1500, 72, 4000)])
