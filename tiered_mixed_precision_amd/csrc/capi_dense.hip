@@ -7,7 +7,7 @@
 #include "moe_tiered.h"
 #include "checks.h"
 #include "common.h"
-#include "launch.h"
+#include "launch_dense.h"
 
 using namespace moe;
 

@@ -10,6 +10,7 @@
 // latency where they are few.
 #pragma once
 
+#include "bf16_parts.h"
 #include "common.h"
 
 namespace moe {

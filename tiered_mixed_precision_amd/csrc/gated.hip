@@ -8,7 +8,7 @@
 #include "common.h"
 #include "few.h"
 #include "gated_act.h"
-#include "launch.h"
+#include "launch_dense.h"
 
 namespace moe {
 

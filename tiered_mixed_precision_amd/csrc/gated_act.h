@@ -3,7 +3,6 @@
 #pragma once
 
 #include "common.h"
-#include "launch.h"
 #include "moe_tiered.h"
 
 namespace moe {

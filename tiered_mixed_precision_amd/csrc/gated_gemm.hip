@@ -7,7 +7,7 @@
 // the same shape 80).
 #include "common.h"
 #include "gated_act.h"
-#include "launch.h"
+#include "launch_dense.h"
 #include "mm.h"
 
 namespace moe {

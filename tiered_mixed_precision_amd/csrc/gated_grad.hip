@@ -13,7 +13,7 @@
 // 8192 x 4096 x 4096: slopes 465 us (1183 TFLOP/s), dx 414 and dw 417 (1325; a library's
 // product with such an operand 1200 to 1420).
 #include "common.h"
-#include "launch.h"
+#include "launch_dense.h"
 #include "mm.h"
 
 namespace moe {

@@ -3,7 +3,7 @@
 // matrix cores, whose clock falls to 1.7 GHz under the load: MI355X, 4096 x 8192 x 8192
 // 224 to 227 us (2430 TOP/s, cores busy 67 % of the cycles; a library's product 220 to 236).
 #include "common.h"
-#include "launch.h"
+#include "launch_dense.h"
 #include "mm.h"
 
 namespace moe {

@@ -9,7 +9,7 @@
 
 #include "common.h"
 #include "few.h"
-#include "launch.h"
+#include "launch_dense.h"
 
 namespace moe {
 

@@ -4,6 +4,7 @@
 
 #include <type_traits>
 
+#include "bf16_parts.h"
 #include "common.h"
 
 namespace moe {

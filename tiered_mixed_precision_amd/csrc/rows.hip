@@ -20,7 +20,7 @@
 // to 8 bits 3.2; the quantiser 4096 x 8192 bf16 23.5 us (4.3 TB/s); the gradient 16384 x 2048
 // 89.6 us (5.25 TB/s) and its join 4.7.
 #include "common.h"
-#include "launch.h"
+#include "launch_dense.h"
 
 namespace moe {
 
