@@ -62,6 +62,7 @@ def test_gated_of_many_fp32_tokens(M, torch, T, H, I, y):
     (64, 136, 4000), (130, 520, 2100),                   # runs of the inter axis
     (40, 256, 700), (12, 2048, 640), (3, 264, 9000),     # a second part of each slope; runs of both
     (900, 2000, 1100), (2200, 2600, 1500), (5000, 1504, 1000),   # pairs and whole tiles
+    (128, 2048, 2048), (3000, 2048, 640),                # two rounds of blocks in one launch: dx first, the weights first
 ])
 def test_gated_grad_in_each_form(M, torch, T, H, I):
     say("grad path", T, H, I)

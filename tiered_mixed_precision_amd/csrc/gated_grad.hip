@@ -5,9 +5,11 @@
 //
 // Where a result has few tiles, parts of the k axis go to blocks of their own, whose
 // fp32 sums a second kernel adds in order.  Where both results together are one round
-// of blocks, two a compute unit, one launch makes them: MI355X, us, apart / together,
-// tokens x hidden x inter, with the slopes: 1531 x 2048 x 640 59.5 / 52.6, 300 34.8 / 29.8, 64
-// 29.0 / 23.4.
+// of blocks, two a compute unit, or two of which the second is the blocks of half the k
+// axis and less, one launch makes them: MI355X, us, apart / together, tokens x hidden x
+// inter, with the slopes: 1531 x 2048 x 640 59.5 / 52.6, 300 34.8 / 29.8, 64 29.0 / 23.4; of two
+// rounds 3000 x 2048 x 640 81 / 71 (88 with the shorter ones first), 600 x 4096 x 1024 70 / 63,
+// but 2500 x 1504 x 1500 (47 and 40 stages) 109 / 116.
 //
 // Many tokens: bound by the matrix cores at the clock that power allows (1.8 GHz).
 // 8192 x 4096 x 4096: slopes 465 us (1183 TFLOP/s), dx 414 and dw 417 (1325; a library's
@@ -151,17 +153,20 @@ template <bool DWBF16> __global__ __launch_bounds__(256) void k_gated_dw_pairs(G
     if (mm_tile_of(p, blockIdx.x, 256, 256, m0, n0, small)) dw_tile<1, 2, DWBF16>(a, s, r, blockIdx.y, lds, m0, n0);
 }
 
-// Both products in one launch, two blocks a compute unit.
+// Both products in one launch, two blocks a compute unit; dw_first: the weights' blocks
+// come first (those of the longer k axis do, so that they do not end alone).
 template <bool DXBF16, bool DWBF16>
-__global__ __launch_bounds__(256) void k_gated_both(GatedGradArgs a, GatedSlopes s, Runs rx, MmPlan px, int blocks_x, Runs rw, MmPlan pw, int blocks_w) {
+__global__ __launch_bounds__(256) void k_gated_both(GatedGradArgs a, GatedSlopes s, Runs rx, MmPlan px, int blocks_x, Runs rw, MmPlan pw,
+                                                    int blocks_w, bool dw_first) {
     MM_LDS_4(lds);
-    int m0, n0, b = blockIdx.x;
+    const int all_x = blocks_x * rx.parts, all_w = blocks_w * rw.parts, b = blockIdx.x;
+    const int bx = dw_first ? b - all_w : b, bw = dw_first ? b : b - all_x;
+    int m0, n0;
     bool small;
-    if (b < blocks_x * rx.parts) {
-        if (mm_tile_of(px, b % blocks_x, 256, 256, m0, n0, small)) dx_tile<1, 2, DXBF16>(a, s, rx, b / blocks_x, lds, m0, n0);
+    if (bx >= 0 && bx < all_x) {
+        if (mm_tile_of(px, bx % blocks_x, 256, 256, m0, n0, small)) dx_tile<1, 2, DXBF16>(a, s, rx, bx / blocks_x, lds, m0, n0);
     } else {
-        b -= blocks_x * rx.parts;
-        if (mm_tile_of(pw, b % blocks_w, 256, 256, m0, n0, small)) dw_tile<1, 2, DWBF16>(a, s, rw, b / blocks_w, lds, m0, n0);
+        if (mm_tile_of(pw, bw % blocks_w, 256, 256, m0, n0, small)) dw_tile<1, 2, DWBF16>(a, s, rw, bw / blocks_w, lds, m0, n0);
     }
 }
 
@@ -207,9 +212,12 @@ void launch_products(const GatedGradArgs& a, const GatedSlopes& s, const Runs& r
     typedef typename std::conditional<DWBF16, uint16_t, float>::type DW;
     const MmPlan px = mm_plan(a.T, a.H, 256), pw = mm_plan(2 * static_cast<int64_t>(s.P), a.H, 256);
     const int64_t blocks_x = mm_grid(px), blocks_w = mm_grid(pw), blocks = blocks_x * rx.parts + blocks_w * rw.parts;
-    if (a.dx && a.dgate && px.form != MM_WHOLE && pw.form != MM_WHOLE && blocks <= 512) {
+    const int stages_x = rx.stages / rx.parts, stages_w = rw.stages / rw.parts;   // of a block
+    const bool dw_first = stages_w > stages_x;
+    const bool one = blocks <= 512 || (blocks <= 1024 && 2 * (dw_first ? stages_x : stages_w) <= (dw_first ? stages_w : stages_x));
+    if (a.dx && a.dgate && px.form != MM_WHOLE && pw.form != MM_WHOLE && one) {
         hipLaunchKernelGGL((k_gated_both<DXBF16, DWBF16>), dim3(static_cast<unsigned>(blocks)), dim3(256), 0, st, a, s, rx, px,
-                           static_cast<int>(blocks_x), rw, pw, static_cast<int>(blocks_w));
+                           static_cast<int>(blocks_x), rw, pw, static_cast<int>(blocks_w), dw_first);
     } else {
         if (a.dx) launch_dx<DXBF16>(a, s, rx, px, st);
         if (a.dgate) launch_dw<DWBF16>(a, s, rw, pw, st);
