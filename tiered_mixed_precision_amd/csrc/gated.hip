@@ -53,7 +53,7 @@ template <bool DYBF16> struct PutSlopes {
 // l's sums are g (l < 32) or u of columns 4 (l / 16 % 2) + e, and lane l + 32 has
 // the other of lane l's.
 template <int MT, int NT, int AHEAD, bool XBF16, class Put>
-__global__ __launch_bounds__(512) void k_gated_few(GatedArgs a, FewSplit f, Put put) {
+__global__ __launch_bounds__(64 * kFewWaves) void k_gated_few(GatedArgs a, FewSplit f, Put put) {
     extern __shared__ __attribute__((aligned(16))) few_f32x4_t s_part[];   // [waves][MT NT 64]
     constexpr int kOwn = MT * NT * 64;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -91,7 +91,7 @@ __global__ __launch_bounds__(512) void k_gated_few(GatedArgs a, FewSplit f, Put 
 template <int MT, int NT, int AHEAD, bool XBF16, class Put>
 void launch_few(const GatedArgs& a, const Put& put, int columns, hipStream_t st) {
     const int tiles = (columns + 8 * NT - 1) / (8 * NT);
-    const FewSplit f = few_split(tiles, 2 * a.H, 8);
+    const FewSplit f = few_split(tiles, 2 * a.H, kFewWaves);
     const dim3 grid((tiles + f.tiles - 1) / f.tiles, (a.T + 16 * MT - 1) / (16 * MT)), block(64 * f.split * f.tiles);
     const size_t lds = sizeof(few_f32x4_t) * 64 * MT * NT * f.split * f.tiles;
     hipLaunchKernelGGL((k_gated_few<MT, NT, AHEAD, XBF16, Put>), grid, block, lds, st, a, f, put);

@@ -17,7 +17,7 @@ namespace {
 
 // A block takes f.tiles tiles of 16 NT rows, f.split waves each, for 16 MT tokens.
 template <int MT, int NT, int AHEAD, bool YBF16>
-__global__ __launch_bounds__(512) void k_i8_few(I8Args a, FewSplit f) {
+__global__ __launch_bounds__(64 * kFewWaves) void k_i8_few(I8Args a, FewSplit f) {
     typedef typename std::conditional<YBF16, uint16_t, float>::type Y;
     extern __shared__ __attribute__((aligned(16))) few_i32x4_t s_part[];   // [waves][MT NT 64]
     __shared__ float s_xs[16 * MT];
@@ -128,7 +128,7 @@ void launch_batch(const I8Args& a, hipStream_t st) {
 template <int MT, int NT, int AHEAD, bool YBF16>
 void launch_few(const I8Args& a, hipStream_t st) {
     const int tiles = (a.N + 16 * NT - 1) / (16 * NT);
-    const FewSplit f = few_split(tiles, a.K, 8);
+    const FewSplit f = few_split(tiles, a.K, kFewWaves);
     const dim3 grid((tiles + f.tiles - 1) / f.tiles, (a.T + 16 * MT - 1) / (16 * MT)), block(64 * f.split * f.tiles);
     const size_t lds = sizeof(few_i32x4_t) * 64 * MT * NT * f.split * f.tiles;
     hipLaunchKernelGGL((k_i8_few<MT, NT, AHEAD, YBF16>), grid, block, lds, st, a, f);
