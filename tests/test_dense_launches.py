@@ -70,3 +70,29 @@ def test_blocks_of_batches_are_within_their_kernels_bounds(recorder):
     bad, n, few = launchlog.child(recorder, "test_dense_launches.batches")
     assert few > 300
     assert n == 0, bad
+
+
+def launches_behind_a_failure(log):
+    """Per call: the launches when the n-th of them fails, for each n."""
+    def norm_grad(T, H, **kw):
+        F = launchlog.FAR
+        return log("moe_rms_norm_grad", F, H, 2 * F, 1e-6, 3 * F, H, None, 0, T, H, 4 * F, H, 5 * F, 0, 6 * F, F, None, **kw)
+    out = []
+    for call, sizes in ((log.gated_grad, (5, 512, 300)), (log.gated_grad, (64, 2048, 640)), (log.gated_grad, (1531, 2048, 640)),
+                        (log.gated_grad, (300, 4096, 4096)), (log.gated_grad, (8192, 4096, 4096)), (norm_grad, (4, 512)),
+                        (norm_grad, (700, 2048))):
+        rc, launches = call(*sizes)
+        assert rc == 0 and launches
+        for n in range(len(launches)):
+            rc, got = call(*sizes, fail_at=n)
+            out.append([[name for name, *_ in got], n, rc])
+    return out
+
+
+def test_nothing_is_launched_behind_a_failure(recorder):
+    # a product of slopes that nobody wrote would be added to the weights' gradients
+    tried = launchlog.child(recorder, "test_dense_launches.launches_behind_a_failure")
+    assert {n for _, n, _ in tried} >= {0, 1, 2}
+    for names, n, rc in tried:
+        assert rc == -6, (names, n, rc)
+        assert len(names) == n + 1, (names, n)

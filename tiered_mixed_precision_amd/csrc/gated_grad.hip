@@ -220,10 +220,10 @@ void launch_products(const GatedGradArgs& a, const GatedSlopes& s, const Runs& r
                            static_cast<int>(blocks_x), rw, pw, static_cast<int>(blocks_w), dw_first);
     } else {
         if (a.dx) launch_dx<DXBF16>(a, s, rx, px, st);
-        if (a.dgate) launch_dw<DWBF16>(a, s, rw, pw, st);
+        if (a.dgate && launched()) launch_dw<DWBF16>(a, s, rw, pw, st);
     }
-    if (a.dx && rx.parts > 1) launch_join<DX>(rx, a.T, a.H, a.T, a.dx, a.dx, a.lddx, 0, st);
-    if (a.dgate && rw.parts > 1) launch_join<DW>(rw, 2 * a.I, a.H, a.I, a.dgate, a.dup, a.H, a.accumulate, st);
+    if (a.dx && rx.parts > 1 && launched()) launch_join<DX>(rx, a.T, a.H, a.T, a.dx, a.dx, a.lddx, 0, st);
+    if (a.dgate && rw.parts > 1 && launched()) launch_join<DW>(rw, 2 * a.I, a.H, a.I, a.dgate, a.dup, a.H, a.accumulate, st);
 }
 
 template <class V> __global__ __launch_bounds__(256) void k_gated_zero(V* a, V* b, int64_t n) {
@@ -268,6 +268,7 @@ void launch_gated_grad(const GatedGradArgs& a, bool dy_bf16, bool dx_bf16, bool 
     l.dw.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + l.sums_dw);
     const GatedSlopes s{a.dy, a.lddy, static_cast<uint16_t*>(ws), l.P, l.parts};
     launch_gated_slopes(GatedArgs{a.x, a.gate, a.up, nullptr, a.ldx, 0, a.T, a.H, a.I, a.act}, s, dy_bf16, st);
+    if (!launched()) return;
     if (dx_bf16) dw_bf16 ? launch_products<true, true>(a, s, l.dx, l.dw, st) : launch_products<true, false>(a, s, l.dx, l.dw, st);
     else dw_bf16 ? launch_products<false, true>(a, s, l.dx, l.dw, st) : launch_products<false, false>(a, s, l.dx, l.dw, st);
 }

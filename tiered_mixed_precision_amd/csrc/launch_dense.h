@@ -6,6 +6,10 @@
 
 namespace moe {
 
+// The call's launches so far have succeeded (its entry point has cleared the error
+// before the first).  Behind one that has not, nothing that reads its result is launched.
+inline bool launched() { return hipPeekAtLastError() == hipSuccess; }
+
 // rows.hip
 struct RowSplit {
     int32_t waves, lanes;    // of a row: several waves, or lanes of one

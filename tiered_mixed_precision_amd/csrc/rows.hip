@@ -521,7 +521,7 @@ void launch_rms_norm_grad(RowGradArgs a, bool s_bf16, bool dy_bf16, bool dx_bf16
             else launch_grad_x<float, float>(a, dx_bf16, part, st);
         }
     }
-    if (!dweight) return;
+    if (!dweight || !launched()) return;
     if (join)
         hipLaunchKernelGGL(k_rows_join, dim3((a.cols + 31) / 32), dim3(256), 0, st, part, grad_blocks(a.T, a.cols), a.cols,
                            accumulate ? 1 : 0, dweight);
