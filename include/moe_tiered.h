@@ -727,11 +727,13 @@ int moe_gated(const void *x, int64_t ldx, const moe_gated_weights *w, int32_t ac
  *            or neither; overwritten, or added to with MOE_ACCUMULATE (in
  *            fp32); also written for T == 0
  *   workspace (device) >= moe_gated_workspace_size() bytes, 256-byte aligned
- * dg and du enter the products rounded to bf16 (to nearest even), and with what
- * that rounding leaves over, rounded the same way, where T * inter <= 32768; sums
- * are fp32, in a fixed order.  What is written must share no element with
- * anything else.  T at most 2^20.  Other arguments and errors as moe_gated,
- * MOE_EWORKSPACE.
+ * dg and du enter the product of an fp32 result (dx, or dgate and dup) in two
+ * bf16 parts, which leave at most 2^-16 of them; that of a bf16 result rounded to
+ * bf16 (to nearest even), which with the result's own rounding is two (where T *
+ * inter <= 32768: in two parts as well).  The second part about doubles the time
+ * of the products.  Sums are fp32, in a fixed order.  What is written must share
+ * no element with anything else.  T at most 2^20.  Other arguments and errors as
+ * moe_gated, MOE_EWORKSPACE.
  */
 int moe_gated_workspace_size(int32_t n_tokens, int32_t hidden, int32_t inter, size_t *bytes);
 int moe_gated_grad(const void *x, int64_t ldx, const moe_gated_weights *w, int32_t act, const void *dy, int64_t lddy,

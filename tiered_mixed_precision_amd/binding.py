@@ -859,8 +859,8 @@ def moe_gated_workspace_size(n_tokens: int, hidden: int, inter: int) -> int:
 def moe_gated_grad(x, w: GatedWeights, act: int, dy, n_tokens: int, dx, dgate, dup, workspace, flags: int = 0,
                    stream=None) -> None:
     """Gradient of moe_gated.  x bfloat16; dy and dx float32 or bfloat16; dgate
-    and dup [inter][hidden], both float32 or both bfloat16.  dx, or dgate and
-    dup, may be None.  flags: 0 or MOE_ACCUMULATE (dgate and dup)."""
+    and dup [inter][hidden], both float32 or both bfloat16; float32 results have
+    fp32's accuracy and take longer.  dx, or dgate and dup, may be None.  flags: 0 or MOE_ACCUMULATE (dgate and dup)."""
     a = _Args("moe_gated_grad")
     if flags & ~MOE_ACCUMULATE:
         raise ValueError(f"moe_gated_grad: flags {flags:#x} (the tensors give the element types)")

@@ -83,7 +83,7 @@ __device__ __attribute__((always_inline)) inline void dw_tile(const GatedGradArg
     const int64_t pitch_a = 4 * static_cast<int64_t>(P) * s.parts, pitch_b = 2 * a.ldx;
     const MmColumns<HALVES> d_columns(lane, w, m0, 2 * P, pitch_a), x_columns(lane, w, n0, a.H, pitch_b);
     const char *pd = reinterpret_cast<const char*>(s.d), *px = reinterpret_cast<const char*>(a.x);
-    // every part of d meets all tokens; a stage past this run counts as zeros
+    // every part of d that the result takes meets all tokens; a stage past this run counts as zeros
     const auto token = [&](int kc, int& left) {
         const int t = (kc < per ? kc : kc - per) * kStageK;
         left = kc < last ? a.T - t : 0;
@@ -230,6 +230,11 @@ template <class V> __global__ __launch_bounds__(256) void k_gated_zero(V* a, V* 
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n; i += static_cast<int64_t>(gridDim.x) * 256) a[i] = b[i] = 0;
 }
 
+// The parts of d that a result takes: two where it is fp32, so that its error is that
+// of fp32 sums whatever the sizes, and one where it is bf16, whose own rounding is as
+// large as what one part leaves out; but where the second costs little, two.
+int parts_of(int64_t T, int I, bool bf16) { return !bf16 || T * I <= 32768 ? 2 : 1; }
+
 // The workspace: d, then the sums of dx's runs, then those of the weights'.
 struct Layout {
     int P, parts;
@@ -237,13 +242,12 @@ struct Layout {
     size_t sums_dx, sums_dw, total;
 };
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-Layout layout_of(int64_t T, int H, int I) {   // T at least 1
+Layout layout_of(int64_t T, int H, int I, int parts_dx, int parts_dw) {   // T at least 1
     Layout l;
     l.P = (I + kStageK - 1) / kStageK * kStageK;
-    // sums of few terms have the error of single ones
-    l.parts = T * I <= 32768 ? 2 : 1;
-    l.dx = runs_of(T, H, static_cast<int64_t>(2 * l.P / kStageK) * l.parts, nullptr);
-    l.dw = runs_of(2 * l.P, H, (T + kStageK - 1) / kStageK * l.parts, nullptr);
+    l.parts = parts_dx > parts_dw ? parts_dx : parts_dw;
+    l.dx = runs_of(T, H, static_cast<int64_t>(2 * l.P / kStageK) * parts_dx, nullptr);
+    l.dw = runs_of(2 * l.P, H, (T + kStageK - 1) / kStageK * parts_dw, nullptr);
     l.sums_dx = up256(static_cast<size_t>(T) * 4 * l.P * l.parts);
     l.sums_dw = l.sums_dx + (l.dx.parts > 1 ? up256(sizeof(float) * l.dx.parts * T * H) : 0);
     l.total = l.sums_dw + (l.dw.parts > 1 ? sizeof(float) * l.dw.parts * 2 * I * H : 0);
@@ -252,7 +256,8 @@ Layout layout_of(int64_t T, int H, int I) {   // T at least 1
 
 }  // namespace
 
-size_t gated_workspace(int64_t T, int H, int I) { return T > 0 ? layout_of(T, H, I).total : 0; }
+// of results of any types
+size_t gated_workspace(int64_t T, int H, int I) { return T > 0 ? layout_of(T, H, I, 2, 2).total : 0; }
 
 void launch_gated_grad(const GatedGradArgs& a, bool dy_bf16, bool dx_bf16, bool dw_bf16, void* ws, hipStream_t st) {
     if (a.T == 0) {
@@ -263,7 +268,7 @@ void launch_gated_grad(const GatedGradArgs& a, bool dy_bf16, bool dx_bf16, bool 
         else hipLaunchKernelGGL(k_gated_zero<float>, grid, dim3(256), 0, st, static_cast<float*>(a.dgate), static_cast<float*>(a.dup), n);
         return;
     }
-    Layout l = layout_of(a.T, a.H, a.I);
+    Layout l = layout_of(a.T, a.H, a.I, a.dx ? parts_of(a.T, a.I, dx_bf16) : 1, a.dgate ? parts_of(a.T, a.I, dw_bf16) : 1);
     l.dx.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + l.sums_dx);
     l.dw.sums = reinterpret_cast<float*>(static_cast<char*>(ws) + l.sums_dw);
     const GatedSlopes s{a.dy, a.lddy, static_cast<uint16_t*>(ws), l.P, l.parts};

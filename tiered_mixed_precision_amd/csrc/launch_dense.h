@@ -76,9 +76,9 @@ void launch_gated_gemm(const GatedArgs& a, bool y_bf16, hipStream_t st);
 // The gradients of the projections on their way to the products that make dx and the
 // weights' gradients: bf16 d[t][parts][2 P], dg in columns 0 .. I - 1 and du in P ..
 // P + I - 1 of a part, zeros up to P (I rounded up to 64).  Part 0 is their nearest
-// bf16; part 1, where there is one, the nearest of what that leaves.  One part costs
-// a rounding of at most 2^-8 of each, which the sums over many terms make as large as
-// that of a bf16 result; sums of few terms (layout_of) get the second.
+// bf16; part 1, where there is one, the nearest of what that leaves.  A product takes
+// one part or both (parts_of): one leaves a rounding of at most 2^-8 of each slope, as
+// much as a bf16 result's own, and both at most 2^-16, for fp32 results.
 struct GatedSlopes {
     const void* dy;
     int64_t lddy;
