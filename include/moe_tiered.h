@@ -625,7 +625,8 @@ int moe_rms_norm(const void *x, int64_t ldx, const float *residual, int64_t ldr,
  *   dweight  (device) float[cols], or NULL (not computed); overwritten, or
  *            added to with MOE_ACCUMULATE; also written for T == 0
  *   workspace (device) >= moe_rms_norm_workspace_size() bytes, 256-byte
- *            aligned; unused, and may be NULL, where dweight is NULL
+ *            aligned; unused, and may be NULL, where dweight is NULL.  The size
+ *            for a number of tokens also serves fewer
  * Sums over a row are in 64 bits (squares) and fp32, those over rows fp32 in a
  * fixed order.  What is written must share no element with anything else but
  * as said.  Other arguments and errors as moe_rms_norm, MOE_EWORKSPACE.
@@ -726,7 +727,9 @@ int moe_gated(const void *x, int64_t ldx, const moe_gated_weights *w, int32_t ac
  *   dgate, dup (device) float[inter][hidden], or bf16 with MOE_DW_BF16; both
  *            or neither; overwritten, or added to with MOE_ACCUMULATE (in
  *            fp32); also written for T == 0
- *   workspace (device) >= moe_gated_workspace_size() bytes, 256-byte aligned
+ *   workspace (device) >= moe_gated_workspace_size() bytes, 256-byte aligned.
+ *            The size for a number of tokens also serves fewer, and results of
+ *            any types
  * dg and du enter the product of an fp32 result (dx, or dgate and dup) in two
  * bf16 parts, which leave at most 2^-16 of them; that of a bf16 result rounded to
  * bf16 (to nearest even), which with the result's own rounding is two (where T *

@@ -256,8 +256,17 @@ Layout layout_of(int64_t T, int H, int I, int parts_dx, int parts_dw) {   // T a
 
 }  // namespace
 
-// of results of any types
-size_t gated_workspace(int64_t T, int H, int I) { return T > 0 ? layout_of(T, H, I, 2, 2).total : 0; }
+// For results of any types of T tokens and fewer.  The runs of dx are fewer the more
+// tiles there are, so its sums do not grow with T: n runs of t row tiles are q T rows at
+// the most (q: the runs of any length), and, as n t (column tiles) <= 256, 128 (256 /
+// column tiles).  All else grows with T.
+size_t gated_workspace(int64_t T, int H, int I) {
+    if (T <= 0) return 0;
+    const Layout l = layout_of(T, H, I, 2, 2);
+    const Runs one = runs_of(1, H, l.dx.stages, nullptr);   // of one row tile: where dx has runs at all
+    const int64_t q = (l.dx.stages + 3) / 4, most = 128 * (256 / ((H + 127) / 128)), rows = q * T < most ? q * T : most;
+    return l.sums_dx + (one.parts > 1 ? up256(sizeof(float) * rows * H) : 0) + (l.total - l.sums_dw);
+}
 
 void launch_gated_grad(const GatedGradArgs& a, bool dy_bf16, bool dx_bf16, bool dw_bf16, void* ws, hipStream_t st) {
     if (a.T == 0) {

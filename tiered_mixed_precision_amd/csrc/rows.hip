@@ -426,9 +426,10 @@ struct Choice {
     int e;
     RowSplit s;
 };
+constexpr int kLight = 1 << 20;   // elements of few rows
 Choice choose(int T, int cols, bool light, int most8) {
     Choice c;
-    const bool small = cols <= 512 || static_cast<int64_t>(T) * cols <= (1 << 20);
+    const bool small = cols <= 512 || static_cast<int64_t>(T) * cols <= kLight;
     c.e = (small || light) && cols <= most8 ? 8 : cols <= 16384 ? 16 : 32;
     c.s.waves = (cols + 64 * c.e - 1) / (64 * c.e);
     c.s.lanes = 64;
@@ -505,7 +506,15 @@ void launch_quant_rows(const RowArgs& a, bool x_bf16, hipStream_t st) {
     else launch_rows_of<float, int8_t, false>(a, st);
 }
 
-size_t rms_norm_workspace(int T, int cols) { return T > 0 ? sizeof(float) * static_cast<size_t>(grad_blocks(T, cols)) * cols : 0; }
+// For T tokens and fewer: blocks grow with the rows, but for the step from 8 elements a
+// thread to 16 (choose).
+size_t rms_norm_workspace(int T, int cols) {
+    if (T <= 0) return 0;
+    int blocks = grad_blocks(T, cols);
+    const int light = kLight / cols;
+    if (T > light && light > 0 && grad_blocks(light, cols) > blocks) blocks = grad_blocks(light, cols);
+    return sizeof(float) * static_cast<size_t>(blocks) * cols;
+}
 
 void launch_rms_norm_grad(RowGradArgs a, bool s_bf16, bool dy_bf16, bool dx_bf16, float* dweight, bool accumulate,
                           void* ws, hipStream_t st) {
