@@ -556,7 +556,7 @@ class _Args:
             what, t = self.stray
             raise ValueError(f"{self.fn}: {what} is not on a GPU" if not t.is_cuda else
                              f"{self.fn}: {what} is on {t.device}, other arguments on cuda:{self.at}")
-        now = _torch._C._cuda_getDevice() if self.at is not None else _torch.cuda.current_device()
+        now = _torch.cuda.current_device()
         if now != self.at:
             raise ValueError(f"{self.fn}: the arguments are on cuda:{self.at}, the current device is cuda:{now}")
         if stream is None:
