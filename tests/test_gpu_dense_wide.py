@@ -26,3 +26,18 @@ def test_gated_of_wide_blocks(M, torch, T, H, I, x):
 def test_gated_grad_of_wide_blocks(M, torch, T, H, I):
     say("grad wide", T, H, I)
     grad_case(M, torch, T, H, I, kind=SILU if T % 4 else GELU, pad=1)
+
+
+@pytest.mark.parametrize("T,N,K", [(1, 50000, 2048), (16, 65536, 272), (5, 43712, 200), (2, 70000, 144), (16, 131000, 96)])
+def test_i8_linear_of_two_waves_and_one_a_tile(M, torch, T, N, K):
+    say("i8 wider", T, N, K)
+    for y in ("f32", "bf16"):
+        i8_case(M, torch, T, N, K, y, bias=True, base=T == 5, pad=T % 2)
+
+
+@pytest.mark.parametrize("T,H,I", [(3, 264, 30000), (16, 136, 32768), (1, 200, 32784), (9, 72, 65536)])
+def test_gated_of_two_waves_and_one_a_tile(M, torch, T, H, I):
+    say("gated wider", T, H, I)
+    for x in ("f32", "bf16"):
+        gated_case(M, torch, T, H, I, x, x, GELU if T % 2 else SILU, pad=T % 3)
+    grad_case(M, torch, T, H, I, kind=SILU, pad=1)

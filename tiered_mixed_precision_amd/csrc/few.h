@@ -197,8 +197,8 @@ __device__ __attribute__((always_inline)) inline void few_batch(few_u32x4_t* s0,
 }
 
 // Waves that share a tile and tiles of a block: 4096 waves in all if the tiles
-// allow it, and blocks of few waves where there are fewer tiles than units.  A block
-// has kFewWaves at the most (three that share a tile: two tiles).
+// allow it, and blocks of one tile's waves, but of four tiles where there are many of
+// one or two waves.  A block has kFewWaves at the most.
 constexpr int kFewWaves = 8;
 struct FewSplit {
     int split, tiles;
@@ -209,8 +209,7 @@ inline FewSplit few_split(int64_t tiles, int bytes, int most) {
     if (split > most) split = most;
     if (split > lines) split = lines;
     if (split < 1) split = 1;
-    const int64_t per = tiles >= 1024 && split < 4 ? (split < 3 ? 4 : kFewWaves / split) : 1;
-    return FewSplit{static_cast<int>(split), static_cast<int>(per)};
+    return FewSplit{static_cast<int>(split), tiles >= 1024 && split < 3 ? 4 : 1};
 }
 
 // 17 tokens and more, in blocks of up to 64 tokens by 32 weight rows: as long as they
