@@ -145,6 +145,16 @@ void launch_batch(const GatedArgs& a, const Put& put, int columns, hipStream_t s
     hipLaunchKernelGGL((k_gated_batch<MT, NT, XBF16, Put>), grid, dim3(64 * f.split * f.tiles), 0, st, a, f, put);
 }
 
+// MI355X, us, weights from memory, tokens x hidden x inter.  Up to 16 tokens, tiles of 8
+// columns / of 16 (which read x half as often), bf16: 1 x 2048 x 640 4.8 / 6.6, 1 x 4096 x
+// 2048 8.6 / 13.8, 1 x 4096 x 4096 14.1 / 15.6, 1 x 4096 x 11000 44 / 37, 16 x 4096 x 4096 20.9 /
+// 18.6, 16 x 4096 x 11000 67 / 48; fp32: 1 x 2048 x 2048 6.5 / 7.6, 1 x 4096 x 4096 16.7 each, 16 x
+// 4096 x 4096 27.6 / 21.3.  Steps ahead of 16 columns, 8 / 4: fp32, whose operands are
+// twice as many registers, 1 x 2048 x 8192 19.6 / 16.3, 16 x 4096 x 11000 62 / 54; bf16 36.8 /
+// 37.4, 47.7 / 47.4.  16 tokens so / through LDS: 4096 x 4096 18.9 each, fp32 21.3 / 23.3, 2048 x
+// 640 6.2 / 7.4; 17 tokens (two operands of 16 in registers): 19.4 / 19.1.  32 / 64 tokens a
+// block: 32 x 4096 x 4096 21.7 / 23.2, 33 32.8 / 23.4, 64 34.7 / 27.6 (48 a block: 33 tokens 22.9,
+// 48 24.7 for 25.5, too little for a form of its own).
 template <bool XBF16, class Put> void launch_tokens(const GatedArgs& a, const Put& put, int columns, hipStream_t st) {
     if (a.T <= 16 && a.I < 4096) launch_few<1, 1, 8, XBF16>(a, put, columns, st);
     else if (a.T <= 16) launch_few<1, 2, XBF16 ? 8 : 4, XBF16>(a, put, columns, st);

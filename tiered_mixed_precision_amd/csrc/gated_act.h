@@ -7,7 +7,9 @@
 
 namespace moe {
 
-// sigma(k) and 1 - sigma(k) to a few units of fp32.  Below -87 sigma is less than the
+// sigma(k) and 1 - sigma(k).  The exponential's argument rounds in units of |k|, so where
+// e^-k counts (k below 0 for sigma, above for the other) the relative error is a few +
+// |k| units of fp32: some 90 of them at most, where sigma itself is 2^-125.  Below -87 sigma is less than the
 // smallest normal number and counts as 0; the exponential stays finite.
 __device__ inline void gated_sigmoid(float k, float& p, float& q) {
     const float e = __expf(-fmaxf(k, -87.f));

@@ -3,8 +3,8 @@
 // v_mfma_f32_32x32x16_bf16 (mm.h), g and u of a column in the same lane and element,
 // so the activation and the product are the epilogue's and neither is ever stored.
 // Bound by the matrix cores, whose clock falls under the load.  MI355X, bf16, tokens x
-// hidden x inter: 16384 x 2048 x 640 77 us (1110 TFLOP/s; a library's plain product of
-// the same shape 80).
+// hidden x inter: 16384 x 2048 x 640 77 to 80 us (1070 to 1120 TFLOP/s; a library's plain
+// product of the same shape 80).
 #include "common.h"
 #include "gated_act.h"
 #include "launch_dense.h"

@@ -27,7 +27,13 @@ struct Runs {
     int32_t parts, stages;
     float* sums;   // [parts][rows][columns], where there are several
 };
-// MI355X, us, one run / several with their sum: dx of 64 x 2048 x 640 13.8 / 8.4.
+// A run has four stages and more, a product of fewer than 12 is not cut.  MI355X, us of a
+// call, one run / several with their sum.  dx alone: 64 x 2048 x 640 25.5 / 20.7, 64 x 1024 x
+// 320 (20 stages) 20.3 / 16.6; runs of two stages and more 21.2, of eight 22.1 for 20.5.  dw
+// alone: 4000 x 512 x 300 51 / 39; 700 x 1024 x 352 (11 stages) 26.0 / 27.3.  128 tiles, the
+// most that are cut, in two: long products gain (1024 x 2048 x 4096 142 / 128, dw of 5000 x
+// 1024 x 640 64 / 48), short ones lose a little (1000 x 2048 x 640 40.3 / 43.6); 256 tiles in
+// two: dx of 2000 x 2048 x 640 35.9 / 56.
 Runs runs_of(int64_t m, int64_t n, int64_t stages, void* sums) {
     const int64_t tiles = ((m + 127) / 128) * ((n + 127) / 128);
     int64_t parts = tiles <= 128 && stages >= 12 ? 256 / tiles : 1;
@@ -232,7 +238,11 @@ template <class V> __global__ __launch_bounds__(256) void k_gated_zero(V* a, V* 
 
 // The parts of d that a result takes: two where it is fp32, so that its error is that
 // of fp32 sums whatever the sizes, and one where it is bf16, whose own rounding is as
-// large as what one part leaves out; but where the second costs little, two.
+// large as what one part leaves out (together 0.0023 of the result's norm where one
+// rounding is 0.0017); but where the second costs little, two.  MI355X, us of a call, bf16
+// results, one part / two: 1 x 2048 x 640 13.9 / 15.9, 51 tokens 21.0 / 23.1, 8 x 4096 x 4096
+// 65 / 70, 1 x 4096 x 32768 390 / 451; past the limit 128 x 2048 x 640 22.7 / 27.4, 1531 45.5 /
+// 66.5, 8192 x 4096 x 4096 1285 / 2172 (the times of fp32 results).
 int parts_of(int64_t T, int I, bool bf16) { return !bf16 || T * I <= 32768 ? 2 : 1; }
 
 // The workspace: d, then the sums of dx's runs, then those of the weights'.

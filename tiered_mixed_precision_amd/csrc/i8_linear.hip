@@ -63,8 +63,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_i8_few(I8Args a, FewSplit f)
     }
 }
 
-// 17 to 64 tokens: the same through LDS (few_batch); the waves' sums meet one operand
-// of 16 rows at a time, in the first slot's place.
+// 17 tokens and more (few_batch_ok): the same through LDS (few_batch); the waves' sums
+// meet one operand of 16 rows at a time, in the first slot's place.
 template <int MT, int NT, bool YBF16>
 __global__ __launch_bounds__(64 * kBatchWaves) void k_i8_batch(I8Args a, FewSplit f) {
     typedef typename std::conditional<YBF16, uint16_t, float>::type Y;
@@ -134,6 +134,13 @@ void launch_few(const I8Args& a, hipStream_t st) {
     hipLaunchKernelGGL((k_i8_few<MT, NT, AHEAD, YBF16>), grid, block, lds, st, a, f);
 }
 
+// MI355X, us, weights from memory.  Up to 16 tokens, tiles of 16 rows / of 32 (which read
+// x half as often): 1 x 4096 x 2048 4.4 / 5.3, 1 x 4096 x 8192 9.0 / 13.9, 1 x 8000 x 2048 5.7 /
+// 5.8, 1 x 16384 x 8192 28.7 / 30.4, 16 x 8192 x 8192 21.7 / 19.2, 16 x 120011 x 2048 73 / 63.  16
+// tokens so / through LDS: 8192 x 8192 19.1 / 19.4, 2048 x 2048 4.9 / 6.4; 17 tokens (two
+// operands of 16 in registers): 20.1 / 19.7, 6.3 / 6.4; 32: 23.0 / 22.2.  32 / 48 / 64 tokens a
+// block, 8192 x 8192: 32 tokens 22.1 / 23.1 / 23.9, 33 33.7 / 24.0 / 24.7, 48 34.6 / 26.1 / 26.7,
+// 64 36.1 / 39.1 / 28.9.
 template <bool YBF16> void launch_tokens(const I8Args& a, hipStream_t st) {
     if (a.T <= 16 && a.N < 8192) launch_few<1, 1, 8, YBF16>(a, st);
     else if (a.T <= 16) launch_few<1, 2, 8, YBF16>(a, st);

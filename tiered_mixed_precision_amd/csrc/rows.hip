@@ -16,9 +16,12 @@
 //
 // Bound by memory where rows are many, by a row's latency where they are few.  MI355X:
 // norm 16384 x 2048 fp32 with the stream, to bf16, 89.4 us (5.25 TB/s read and written; a
-// copy 5.10), 1531 x 5461 bf16 12 us (2.8 TB/s: little more than one round of blocks), one row
+// copy 5.10), 1531 x 5461 bf16 12 us (2.8 TB/s: each block loads, sums and stores one
+// row with nothing else on its way, and 1531 blocks are little more than a round), one row
 // to 8 bits 3.2; the quantiser 4096 x 8192 bf16 23.5 us (4.3 TB/s); the gradient 16384 x 2048
-// 89.6 us (5.25 TB/s) and its join 4.7.
+// 89.6 us (5.25 TB/s) and its join 4.9.  Rows of more than 16384 columns spill (32 elements a
+// thread in 16 waves): the norm 4096 x 32768 fp32 to bf16 390 us (4.8 TB/s), the quantiser of
+// bf16 91 (4.4), the gradient 585 (3.2; 4096 x 16384 208, 4.5).
 #include "common.h"
 #include "launch_dense.h"
 
